@@ -171,7 +171,8 @@ def _plain_mm(s):
 
 def _plain_quant(x):
     x = x.float()
-    scale = x.abs().amax(dim=1, keepdim=True) / 127.0
+    most = x.abs().amax(dim=1, keepdim=True)
+    scale = most / torch.full_like(most, 127.0)  # a quotient: a Python number would be multiplied by its reciprocal
     return torch.where(scale > 0, torch.round(x / scale), torch.zeros_like(x)).clamp(-127, 127), scale
 
 
@@ -296,7 +297,8 @@ def exact(case, seed):
         # by definition the scale and the quotient are 32-bit numbers (a bf16 row often holds half its own
         # largest magnitude, whose quotient 63.5 is a tie), and the code is the integer nearest to the latter
         x = x.to(torch.float32)
-        scale = x.abs().max(dim=1).values[:, None] / 127.0
+        most = x.abs().max(dim=1).values[:, None]
+        scale = torch.true_divide(most, torch.full_like(most, 127.0))
         return torch.nan_to_num(torch.round(x / scale), nan=0.0).clamp(-127, 127).to(d), scale.to(d)
 
     def product(x, w, ws):
