@@ -139,6 +139,19 @@ def lib() -> ctypes.CDLL:
         L.beam_moe_expert_rows.argtypes = [ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, ctypes.c_int64, _vp, _vp,
                                            _vp, _vp, _vp, _vp, _vp, ctypes.c_size_t, _vp]
         L.beam_moe_combine.argtypes = [_cfgp, ctypes.c_int64, _vp, _vp, _vp, _vp, _vp]
+        _i32, _i64, _int = ctypes.c_int32, ctypes.c_int64, ctypes.c_int
+        L.beam_moe_grouped_mm.argtypes = [_i32, _i64, _i32, _i32, _int, _vp, _i64, _vp, _vp, _int, _vp, _i64, _vp]
+        L.beam_moe_grouped_mm_dgrad.argtypes = L.beam_moe_grouped_mm.argtypes
+        L.beam_moe_grouped_mm_wgrad_workspace_size.argtypes = [_i32, _i64, _i32, _i32]
+        L.beam_moe_grouped_mm_wgrad_workspace_size.restype = ctypes.c_size_t
+        L.beam_moe_grouped_mm_wgrad.argtypes = [_i32, _i64, _i32, _i32, _int, _vp, _i64, _vp, _i64, _vp, _int, _vp,
+                                                _int, _vp, ctypes.c_size_t, _vp]
+        L.beam_moe_quant_i8_rows.argtypes = [_i64, _i32, _int, _vp, _i64, _vp, _vp, _vp]
+        L.beam_moe_grouped_mm_i8.argtypes = [_i32, _i64, _i32, _i32, _vp, _vp, _vp, _vp, _vp, _int, _vp, _i64, _vp]
+        L.beam_moe_swiglu.argtypes = [_i64, _i32, _int, _vp, _i64, _vp, _i64, _vp, _i64, _vp]
+        L.beam_moe_swiglu_backward.argtypes = [_i64, _i32, _int, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _vp,
+                                               _i64, _vp]
+        L.beam_moe_swiglu_i8.argtypes = [_i64, _i32, _int, _vp, _i64, _vp, _i64, _vp, _vp, _vp]
         L.beam_moe_device_status.argtypes = [_vp]
         L.beam_moe_selftest_timeout.argtypes = [ctypes.c_int64, _vp]
         L.beam_moe_strerror.argtypes = [ctypes.c_int]
@@ -148,7 +161,9 @@ def lib() -> ctypes.CDLL:
                      "beam_moe_forward_fp8", "beam_moe_experts_nvfp4", "beam_moe_forward_nvfp4",
                      "beam_moe_device_status", "beam_moe_gather_rows", "beam_moe_experts_mxfp8", "beam_moe_forward_mxfp8",
                      "beam_moe_experts_w4a4", "beam_moe_forward_w4a4", "beam_moe_expert_rows", "beam_moe_combine",
-                     "beam_moe_selftest_timeout"):
+                     "beam_moe_selftest_timeout", "beam_moe_grouped_mm", "beam_moe_grouped_mm_dgrad",
+                     "beam_moe_grouped_mm_wgrad", "beam_moe_quant_i8_rows", "beam_moe_grouped_mm_i8",
+                     "beam_moe_swiglu", "beam_moe_swiglu_backward", "beam_moe_swiglu_i8"):
             getattr(L, name).restype = ctypes.c_int
         _lib = L
     return _lib
@@ -615,6 +630,235 @@ def dense_swiglu(x, w_gate, w_up, w_down, y=None, ws=None, stream=None):
     _check(lib().beam_moe_dense_swiglu(H, I, T, _ptr(x), _ptr(w_gate), _ptr(w_up), _ptr(w_down), _ptr(y), _ptr(ws),
                                        ws.numel(), _stream(stream)), "beam_moe_dense_swiglu")
     return y
+
+
+# ---- the experts' steps as operators of their own, with their gradients ---------------------------
+# Matrices over rows may be strided (unit column stride, rows on 16-byte boundaries), every other tensor is
+# contiguous.  A call runs on its tensors' device, on `stream` (default: that device's current stream).
+TYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+_HALF = (torch.bfloat16, torch.float16)
+
+
+def _rows(t, name: str, dtypes, device=None, shape=None) -> torch.Tensor:
+    """Checks a [rows, width] operand."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor (there is no CPU path)")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} must be one of {[str(d) for d in dtypes]}, got {t.dtype}")
+    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError(f"{name} must be a matrix with contiguous rows")
+    if t.shape[0] > 1 and t.stride(0) < t.shape[1]:
+        raise ValueError(f"{name} has overlapping rows (row stride {t.stride(0)} < {t.shape[1]})")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    return t
+
+
+def _ld(t: torch.Tensor) -> int:
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def _on(t, name: str, dtype, shape, device):
+    """_dev, on `device`."""
+    _dev(t, name, dtype, shape)
+    if t is not None and t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    return t
+
+
+def _out_rows(out, name: str, dtypes, default, R: int, width: int, device) -> torch.Tensor:
+    if out is None:
+        return torch.empty(R, width, dtype=default, device=device)
+    return _rows(out, name, dtypes, device, (R, width))
+
+
+def _run(where: str, device, stream, *args, scratch=None):
+    """Calls entry point `where` with `args` and the stream, on `device`."""
+    if stream is None:
+        handle = torch.cuda.current_stream(device).cuda_stream
+    else:
+        handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+        if scratch is not None:  # allocated here, used there: its memory stays taken until that stream is done
+            scratch.record_stream(stream if isinstance(stream, torch.cuda.Stream)
+                                  else torch.cuda.ExternalStream(handle, device=device))
+    fn = getattr(lib(), where)
+    if torch.cuda.current_device() == device.index:
+        code = fn(*args, handle)
+    else:
+        with torch.cuda.device(device):
+            code = fn(*args, handle)
+    if code != OK:
+        raise BeamMoeError(code, where)
+
+
+def _groups_of(offsets, E: int, device):
+    """The offsets' pointer: int64 [E + 1], or None for one group of all rows."""
+    if offsets is None:
+        if E != 1:
+            raise ValueError(f"offsets may be left out with one expert only, got {E}")
+        return None
+    _on(offsets, "offsets", torch.int64, (E + 1,), device)
+    return offsets.data_ptr()
+
+
+def _weights3(w, name: str, dtype, device):
+    """[E, N, K] weights; a matrix [N, K] is one expert."""
+    if isinstance(w, torch.Tensor) and w.dim() == 2:
+        w = w.unsqueeze(0)
+    _on(w, name, dtype, None, device)
+    if w.dim() != 3:
+        raise ValueError(f"{name} must be [experts, N, K] or [N, K], got {tuple(w.shape)}")
+    return w
+
+
+def _out_type(out, out_dtype, default):
+    """The result's type: out_dtype, else that of `out`, else `default`."""
+    d = out_dtype if out_dtype is not None else (out.dtype if isinstance(out, torch.Tensor) else default)
+    if d not in TYPES:
+        raise TypeError(f"out_dtype must be one of {[str(k) for k in TYPES]}, got {d}")
+    return d
+
+
+def grouped_mm(x, w, offsets=None, out=None, out_dtype=None, stream=None) -> torch.Tensor:
+    """out[r] = w[e] x[r] for the rows offsets[e] <= r < offsets[e + 1] of each expert e.
+
+    x [R, K] and w [E, N, K] bf16 or fp16 (or w [N, K] without offsets: one expert that takes every row);
+    offsets [E + 1] int64 on the device (permute()'s); out [R, N] in x's type or fp32.  Rows of no expert
+    are not written."""
+    _rows(x, "x", _HALF)
+    w = _weights3(w, "w", x.dtype, x.device)
+    (R, K), (E, N, Kw) = x.shape, w.shape
+    if K != Kw:
+        raise ValueError(f"x has {K} columns, w expects {Kw}")
+    od = _out_type(out, out_dtype, x.dtype)
+    out = _out_rows(out, "out", (od,), od, R, N, x.device)
+    _run("beam_moe_grouped_mm", x.device, stream, E, R, K, N, TYPES[x.dtype], x.data_ptr(), _ld(x),
+         _groups_of(offsets, E, x.device), w.data_ptr(), TYPES[od], out.data_ptr(), _ld(out))
+    return out
+
+
+def grouped_mm_dgrad(dy, w, offsets=None, out=None, out_dtype=None, stream=None) -> torch.Tensor:
+    """Gradient of grouped_mm in x: dx[r] = w[e]^T dy[r]; dy [R, N], w [E, N, K] (or [N, K]) -> [R, K]."""
+    _rows(dy, "dy", _HALF)
+    w = _weights3(w, "w", dy.dtype, dy.device)
+    (R, N), (E, Nw, K) = dy.shape, w.shape
+    if N != Nw:
+        raise ValueError(f"dy has {N} columns, w expects {Nw}")
+    od = _out_type(out, out_dtype, dy.dtype)
+    out = _out_rows(out, "out", (od,), od, R, K, dy.device)
+    _run("beam_moe_grouped_mm_dgrad", dy.device, stream, E, R, K, N, TYPES[dy.dtype], dy.data_ptr(), _ld(dy),
+         _groups_of(offsets, E, dy.device), w.data_ptr(), TYPES[od], out.data_ptr(), _ld(out))
+    return out
+
+
+def grouped_mm_wgrad(dy, x, offsets=None, out=None, out_dtype=None, accumulate: bool = False, ws=None,
+                     stream=None) -> torch.Tensor:
+    """Gradient of grouped_mm in w: dw[e] = sum over its rows of dy[r]^T x[r] -> [E, N, K], zeros for an
+    expert without rows.  accumulate=True adds to `out` (fp32) instead.  Without offsets: one expert
+    (E = 1) that takes every row."""
+    _rows(dy, "dy", _HALF)
+    _rows(x, "x", (dy.dtype,), dy.device)
+    (R, N), K = dy.shape, x.shape[1]
+    if x.shape[0] != R:
+        raise ValueError(f"dy has {R} rows, x {x.shape[0]}")
+    E = 1 if offsets is None else offsets.numel() - 1
+    od = _out_type(out, out_dtype, dy.dtype)
+    if out is None:
+        if accumulate:
+            raise ValueError("accumulate needs out, the fp32 gradient to add to")
+        out = torch.empty(E, N, K, dtype=od, device=dy.device)
+    _on(out, "out", od, (E, N, K) if out.dim() == 3 or E != 1 else (N, K), dy.device)
+    need = int(lib().beam_moe_grouped_mm_wgrad_workspace_size(E, R, K, N))
+    scratch = None
+    if ws is None:
+        if need:
+            ws = scratch = torch.empty(need, dtype=torch.uint8, device=dy.device)
+    else:
+        _on(ws, "ws", torch.uint8, None, dy.device)
+    _run("beam_moe_grouped_mm_wgrad", dy.device, stream, E, R, K, N, TYPES[dy.dtype], dy.data_ptr(), _ld(dy),
+         x.data_ptr(), _ld(x), _groups_of(offsets, E, dy.device), TYPES[od], out.data_ptr(), int(bool(accumulate)),
+         None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel(), scratch=scratch)
+    return out
+
+
+def _codes(q, scale, R: int, K: int, device):
+    q = torch.empty(R, K, dtype=torch.int8, device=device) if q is None else q
+    scale = torch.empty(R, dtype=torch.float32, device=device) if scale is None else scale
+    _on(q, "q", torch.int8, (R, K), device)
+    _on(scale, "scale", torch.float32, (R,), device)
+    return q, scale
+
+
+def quant_i8_rows(x, q=None, scale=None, stream=None):
+    """(q [R, K] int8, scale [R] fp32): scale = max|x[r]| / 127, q = x / scale to the nearest integer."""
+    _rows(x, "x", tuple(TYPES))
+    R, K = x.shape
+    q, scale = _codes(q, scale, R, K, x.device)
+    _run("beam_moe_quant_i8_rows", x.device, stream, R, K, TYPES[x.dtype], x.data_ptr(), _ld(x), q.data_ptr(),
+         scale.data_ptr())
+    return q, scale
+
+
+def grouped_mm_i8(q, row_scale, w, channel_scale, offsets=None, out=None, out_dtype=None, stream=None) -> torch.Tensor:
+    """grouped_mm of INT8 codes: out[r, n] = (q[r] . w[e, n]) * row_scale[r] * channel_scale[e, n].
+
+    q [R, K] int8 and row_scale [R] fp32 (quant_i8_rows), w [E, N, K] int8 and channel_scale [E, N] fp32 (or
+    [N, K] and [N]); out [R, N] bf16 (default), fp16 or fp32."""
+    if not isinstance(q, torch.Tensor) or q.dim() != 2:
+        raise TypeError("q must be a CUDA int8 matrix (there is no CPU path)")
+    R, K = q.shape
+    device = q.device
+    _dev(q, "q", torch.int8)
+    w = _weights3(w, "w", torch.int8, device)
+    E, N, Kw = w.shape
+    if K != Kw:
+        raise ValueError(f"q has {K} columns, w expects {Kw}")
+    if isinstance(channel_scale, torch.Tensor) and channel_scale.dim() == 1:
+        channel_scale = channel_scale.unsqueeze(0)
+    _on(row_scale, "row_scale", torch.float32, (R,), device)
+    _on(channel_scale, "channel_scale", torch.float32, (E, N), device)
+    od = _out_type(out, out_dtype, torch.bfloat16)
+    out = _out_rows(out, "out", (od,), od, R, N, device)
+    _run("beam_moe_grouped_mm_i8", device, stream, E, R, K, N, q.data_ptr(), row_scale.data_ptr(),
+         _groups_of(offsets, E, device), w.data_ptr(), channel_scale.data_ptr(), TYPES[od], out.data_ptr(), _ld(out))
+    return out
+
+
+def swiglu(g, u, out=None, stream=None) -> torch.Tensor:
+    """SiLU(g) * u over [R, I] (bf16, fp16 or fp32); `out` may be g or u."""
+    _rows(g, "g", tuple(TYPES))
+    R, I = g.shape
+    _rows(u, "u", (g.dtype,), g.device, (R, I))
+    out = _out_rows(out, "out", (g.dtype,), g.dtype, R, I, g.device)
+    _run("beam_moe_swiglu", g.device, stream, R, I, TYPES[g.dtype], g.data_ptr(), _ld(g), u.data_ptr(), _ld(u),
+         out.data_ptr(), _ld(out))
+    return out
+
+
+def swiglu_backward(dh, g, u, dg=None, du=None, stream=None):
+    """Gradients (dg, du) of swiglu; dg and du may be any two of the inputs."""
+    _rows(g, "g", tuple(TYPES))
+    R, I = g.shape
+    _rows(u, "u", (g.dtype,), g.device, (R, I))
+    _rows(dh, "dh", (g.dtype,), g.device, (R, I))
+    dg = _out_rows(dg, "dg", (g.dtype,), g.dtype, R, I, g.device)
+    du = _out_rows(du, "du", (g.dtype,), g.dtype, R, I, g.device)
+    _run("beam_moe_swiglu_backward", g.device, stream, R, I, TYPES[g.dtype], dh.data_ptr(), _ld(dh), g.data_ptr(),
+         _ld(g), u.data_ptr(), _ld(u), dg.data_ptr(), _ld(dg), du.data_ptr(), _ld(du))
+    return dg, du
+
+
+def swiglu_i8(g, u, q=None, scale=None, stream=None):
+    """quant_i8_rows(SiLU(g) * u) in one pass, the product kept in fp32: (q [R, I] int8, scale [R] fp32)."""
+    _rows(g, "g", tuple(TYPES))
+    R, I = g.shape
+    _rows(u, "u", (g.dtype,), g.device, (R, I))
+    q, scale = _codes(q, scale, R, I, g.device)
+    _run("beam_moe_swiglu_i8", g.device, stream, R, I, TYPES[g.dtype], g.data_ptr(), _ld(g), u.data_ptr(), _ld(u),
+         q.data_ptr(), scale.data_ptr())
+    return q, scale
 
 
 STAGES = ("router", "dispatch", "gather", "gate_up_swiglu", "down", "combine")

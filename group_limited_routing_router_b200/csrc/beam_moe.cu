@@ -1540,3 +1540,7 @@ int beam_moe_combine(const beam_moe_config *cfg, int64_t T, const float *o_rows,
 }
 
 }  // extern "C"
+
+// ------------------------------------------------------------------------------------------------
+// The experts' products, their gradients, the INT8 products and SwiGLU as operators of their own.
+#include "ragged_api.cuh"

@@ -1,0 +1,1076 @@
+// Matrix products grouped by expert over ragged rows, as operators of their own (the expert half of
+// the layer fuses its two; these are for training and for callers that compose their own experts).
+// Group e owns rows offsets[e] <= r < offsets[e + 1]:
+//   forward   out[r, n] = sum_k x[r, k] w[e, n, k]
+//   dgrad     dx[r, k]  = sum_n dy[r, n] w[e, n, k]
+//   wgrad     dw[e, n, k] (+)= sum_{r in e} dy[r, n] x[r, k]
+//   INT8      out[r, n] = (sum_k q[r, k] wq[e, n, k]) * row_scale[r] * channel_scale[e, n]
+// bf16 / fp16 operands (one type per call; the MMA's type field is a run-time value) with FP32
+// accumulation, or INT8 operands with exact INT32 accumulation.
+//
+// Forward and dgrad are swap-AB: the MMA's M side walks the output features (weight rows in the
+// forward pass, weight columns in dgrad), its N side the group's rows, rounded up to 16 (INT8 pairs:
+// 32), so a group of a few rows wastes little and a weight byte crosses HBM once per token tile.
+// dgrad reads the same [E, N, K] weights: their tile is the MMA's MN-major A operand, so no
+// transposed copy of the weights exists.  wgrad contracts over the rows: both operands are MN-major.
+//
+// Accumulation.  The tensor core's FP32 accumulator rounds toward zero at each instruction (measured
+// on 5120-long sums: 1e-5 relative, all toward zero), so long sums are cut into segments of `seg_kb`
+// k-steps: each segment accumulates in its own TMEM slot and the epilogue adds the segments in FP32
+// registers with round-to-nearest, while the next segment's products run in the other slot.
+//
+// Every mbarrier wait is bounded (status word BEAM_MOE_ERR_DEVICE_TIMEOUT on expiry); offsets that do
+// not ascend within [0, R] set BEAM_MOE_ERR_BAD_INDEX and nothing is written; no load uses multicast.
+#pragma once
+
+#include <cuda_fp16.h>
+
+#include "gemm_2sm.cuh"
+#include "gemm_mx8.cuh"
+
+namespace beam {
+
+constexpr int kRgThreads = 320;       // warp 0 TMA, warp 1 MMA, warps 2..9 epilogue (pairs)
+constexpr int kRgOperand = 16384;     // one staged operand tile: 128 rows of 128 bytes
+constexpr int kRgRowBytes = 128;      // contraction bytes per k-step (64 16-bit or 128 8-bit elements)
+
+struct RaggedParams {
+    const int64_t *offsets;      // [E + 1], or NULL: one group of all R rows
+    void *out;
+    int64_t ldo;                 // output row stride, elements (forward, dgrad)
+    int64_t R;
+    int E;
+    int M;                       // output features (forward: N, dgrad: K)
+    int n_kb;                    // k-steps of 128 bytes over the contraction
+    int seg_kb;                  // k-steps per accumulation segment
+    int out_type;                // BEAM_MOE_BF16 / F16 / F32
+    uint32_t idesc;              // instruction descriptor without N
+    int weights_once;            // 1: each weight tile is read once per call -> L2 evict-first
+    const float *row_scale;      // INT8: [R]
+    const float *channel_scale;  // INT8: [E, M]
+    long long timeout;
+};
+
+// ---- tcgen05 pieces ------------------------------------------------------------------------------
+// MN-major operand written by TMA with 128-byte swizzling: boxes of 64 MN elements (128 bytes) by 64
+// contraction rows; 8-row groups are 1024 B apart (stride byte offset), the next 64 MN elements one
+// box = 8192 B further (leading byte offset).  One instruction takes 16 contraction rows: 2048 B.
+__device__ __forceinline__ uint64_t umma_desc_mn_sw128(uint32_t smem_addr) {
+    uint64_t d = 0;
+    d |= static_cast<uint64_t>((smem_addr >> 4) & 0x3FFFu);
+    d |= static_cast<uint64_t>(8192u >> 4) << 16;
+    d |= static_cast<uint64_t>(1024u >> 4) << 32;
+    d |= static_cast<uint64_t>(1u) << 46;
+    d |= static_cast<uint64_t>(2u) << 61;
+    return d;
+}
+__device__ __forceinline__ void umma_i8(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                        uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::i8 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+__device__ __forceinline__ void umma_i8_pair(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                             uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::i8 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+__device__ __forceinline__ uint32_t idesc_with_n(uint32_t idesc, int n) {
+    return idesc | (static_cast<uint32_t>(n >> 3) << 17);
+}
+
+// mbar_wait whose acquire covers the other CTAs of the cluster (they arrive with release.cluster).
+__device__ __forceinline__ bool mbar_wait_cluster(uint64_t *bar, uint32_t parity, long long timeout) {
+    const long long t0 = clock64();
+    while (true) {
+        uint32_t ok;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}\n"
+            : "=r"(ok)
+            : "r"(smem_u32(bar)), "r"(parity), "r"(kWaitSuspendNs)
+            : "memory");
+        if (ok) return true;
+        if (clock64() - t0 > timeout) {
+            set_status(BEAM_MOE_ERR_DEVICE_TIMEOUT);
+            return false;
+        }
+    }
+}
+
+// ---- groups --------------------------------------------------------------------------------------
+__device__ __forceinline__ int64_t group_begin(const RaggedParams &p, int e) { return p.offsets ? p.offsets[e] : 0; }
+__device__ __forceinline__ int group_rows(const RaggedParams &p, int e) {
+    return static_cast<int>(p.offsets ? p.offsets[e + 1] - p.offsets[e] : p.R);
+}
+
+// Exclusive prefix of the groups' item counts in tile_start[0..E], n_mt items per BN rows of a group
+// (WGRAD: n_mt items per group, `skip_empty` leaving out groups without rows).  Offsets that do not
+// ascend within [0, R] give no items at all.  Contains __syncthreads; E <= 256 <= blockDim.x.
+template <bool WGRAD>
+__device__ __forceinline__ void ragged_prefix(const RaggedParams &p, int n_mt, int BN, bool skip_empty,
+                                              int *tile_start) {
+    __shared__ int warp_tot[32];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int e = threadIdx.x;
+    int v = 0, bad = 0;
+    if (e < p.E) {
+        const int64_t lo = p.offsets ? p.offsets[e] : 0, hi = p.offsets ? p.offsets[e + 1] : p.R;
+        bad = lo < 0 || hi < lo || hi > p.R;
+        const int64_t rows = bad ? 0 : hi - lo;
+        if (WGRAD) v = (skip_empty && rows == 0) ? 0 : n_mt;
+        else v = n_mt * static_cast<int>((rows + BN - 1) / BN);
+    }
+    bad = __syncthreads_or(bad);
+    if (bad) v = 0;
+    if (bad && blockIdx.x == 0 && threadIdx.x == 0) set_status(BEAM_MOE_ERR_BAD_INDEX);
+    int incl = v;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const int o = __shfl_up_sync(0xffffffffu, incl, off);
+        if (lane >= off) incl += o;
+    }
+    if (lane == 31) warp_tot[warp] = incl;
+    __syncthreads();
+    int base = 0;
+    for (int w = 0; w < warp; ++w) base += warp_tot[w];
+    if (e < p.E) tile_start[e] = base + incl - v;
+    if (e == p.E - 1) tile_start[p.E] = base + incl;
+}
+
+__device__ __forceinline__ int find_group(int item, const int *tile_start, int E) {
+    int lo = 0, hi = E - 1;  // largest e with tile_start[e] <= item
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (tile_start[mid] <= item) lo = mid;
+        else hi = mid - 1;
+    }
+    return lo;
+}
+
+// Forward / dgrad item: feature tile mt, row tile nt of group e; ROUND is the MMA's step in N.
+template <int BN, int ROUND>
+__device__ __forceinline__ Item ragged_item(int item, const int *tile_start, const RaggedParams &p) {
+    Item it;
+    it.e = find_group(item, tile_start, p.E);
+    const int rows = group_rows(p, it.e);
+    const int n_nt = (rows + BN - 1) / BN;
+    const int local = item - tile_start[it.e];
+    it.mt = local / n_nt;
+    it.nt = local - it.mt * n_nt;
+    it.n_valid = min(BN, rows - it.nt * BN);
+    it.n_mma = (it.n_valid + ROUND - 1) / ROUND * ROUND;
+    it.row0 = group_begin(p, it.e) + static_cast<int64_t>(it.nt) * BN;
+    return it;
+}
+
+// ---- output ----------------------------------------------------------------------------------------
+// Two values to a pair of 16-bit floats, nearest even.
+template <int TYPE>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+    if constexpr (TYPE == BEAM_MOE_F16) {
+        const __half2 v = __floats2half2_rn(lo, hi);
+        return *reinterpret_cast<const uint32_t *>(&v);
+    } else {
+        const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+        return *reinterpret_cast<const uint32_t *>(&v);
+    }
+}
+
+// Feature m (this lane; M and the lane pairing make m and m ^ 1 valid together) of rows c..c+15.  16-bit
+// outputs: neighbouring lanes exchange every other row so that each stores a pair of features.
+template <int TYPE>
+__device__ __forceinline__ void store_cols(const RaggedParams &p, const Item &it, int c, int m, const float (&v)[16]) {
+    const int lane = threadIdx.x & 31;
+    if constexpr (TYPE == BEAM_MOE_F32) {
+        float *o = reinterpret_cast<float *>(p.out) + (it.row0 + c) * p.ldo + m;
+#pragma unroll
+        for (int j = 0; j < 16; ++j)
+            if (c + j < it.n_valid && m < p.M) o[j * p.ldo] = v[j];
+    } else {
+        const int odd = lane & 1;
+        uint16_t *o = reinterpret_cast<uint16_t *>(p.out) + (it.row0 + c) * p.ldo + (m & ~1);
+#pragma unroll
+        for (int j = 0; j < 16; j += 2) {
+            const float got = __shfl_xor_sync(0xffffffffu, odd ? v[j] : v[j + 1], 1);
+            const uint32_t pr = odd ? pack2<TYPE>(got, v[j + 1]) : pack2<TYPE>(v[j], got);
+            if (c + j + odd < it.n_valid && m < p.M) *reinterpret_cast<uint32_t *>(o + (j + odd) * p.ldo) = pr;
+        }
+    }
+}
+
+// The epilogue's value of an accumulator: INT8 sums take their channel's and row's scale in FP32.
+template <bool I8>
+__device__ __forceinline__ float ragged_value(const RaggedParams &p, uint32_t acc, float channel, float row) {
+    return I8 ? static_cast<float>(static_cast<int32_t>(acc)) * (channel * row) : __uint_as_float(acc);
+}
+
+// ---- forward / dgrad on CTA pairs ------------------------------------------------------------------
+// The pair engine of gemm_2sm.cuh for one product: a pair computes 256 features x up to 256 rows; CTA r
+// stages features 128 r.. and half of the rows.  Stage = 16 KB + 16 KB, 7 stages, two TMEM slots of 256
+// columns, so that a segment's or an item's epilogue always overlaps the next one's products.
+constexpr int kRpStages = 7;
+constexpr int kRpBN = 256;
+constexpr int kRpBox = 32;  // rows per B box
+constexpr int kRpBarOff = kRpStages * 2 * kRgOperand;
+constexpr int kRpTileOff = kRpBarOff + 256;
+constexpr int kRpSmem = 1024 + kRpTileOff + 4 * (kPmMaxE + 1) + 64;
+static_assert(8 * (2 * kRpStages + 2 * 2 + 1) + 4 <= 256, "barrier area");
+static_assert(kRpSmem + 128 <= 232448, "shared memory per CTA (dynamic + the 128 static bytes)");
+
+// Adds `n_valid` accumulator columns of this warp's share (chunks of 16 at 16 sub + 32 i) to acc.
+template <bool I8, int CHUNKS>
+__device__ __forceinline__ void add_segment(uint32_t t, int sub, int stride, int n_valid, bool first,
+                                            uint32_t (&acc)[CHUNKS][16]) {
+    if (first) {
+#pragma unroll
+        for (int i = 0; i < CHUNKS; ++i)
+            if (16 * sub + stride * i < n_valid) tmem_ld16(t + 16 * sub + stride * i, acc[i]);  // warp-uniform
+        tmem_ld_wait();
+    } else {
+#pragma unroll
+        for (int i = 0; i < CHUNKS; ++i)
+            if (16 * sub + stride * i < n_valid) {
+                uint32_t r[16];
+                tmem_ld16(t + 16 * sub + stride * i, r);
+                tmem_ld_wait();
+#pragma unroll
+                for (int j = 0; j < 16; ++j)
+                    acc[i][j] = I8 ? acc[i][j] + r[j]
+                                   : __float_as_uint(__uint_as_float(acc[i][j]) + __uint_as_float(r[j]));
+            }
+    }
+}
+
+template <bool I8, int TYPE, int CHUNKS>
+__device__ __forceinline__ void store_item(const RaggedParams &p, const Item &it, int sub, int m,
+                                           const uint32_t (&acc)[CHUNKS][16]) {
+    const float channel = (I8 && m < p.M) ? __ldg(p.channel_scale + static_cast<int64_t>(it.e) * p.M + m) : 1.0f;
+#pragma unroll
+    for (int i = 0; i < CHUNKS; ++i) {
+        const int c = 16 * sub + 32 * i;
+        if (c < it.n_valid) {  // warp-uniform
+            float v[16];
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+                const float row = (I8 && c + j < it.n_valid) ? __ldg(p.row_scale + it.row0 + c + j) : 1.0f;
+                v[j] = ragged_value<I8>(p, acc[i][j], channel, row);
+            }
+            store_cols<TYPE>(p, it, c, m, v);
+        }
+    }
+}
+
+template <bool I8, bool A_MN>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kRgThreads, 1)
+    ragged_pair_kernel(const __grid_constant__ CUtensorMap tm_w,  // weights [E][N][K]
+                       const __grid_constant__ CUtensorMap tm_b,  // rows [R][contraction], kRpBox-row box
+                       const RaggedParams p) {
+    constexpr int kRound = I8 ? 32 : 16;
+    extern __shared__ uint8_t gemm_smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(gemm_smem_raw) + 1023) & ~uintptr_t(1023));
+    uint64_t *full = reinterpret_cast<uint64_t *>(smem + kRpBarOff);
+    uint64_t *empty = full + kRpStages;
+    uint64_t *acc_full = empty + kRpStages;
+    uint64_t *acc_empty = acc_full + 2;
+    uint64_t *drain = acc_empty + 2;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drain + 1);
+    int *tile_start = reinterpret_cast<int *>(smem + kRpTileOff);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_ctarank();
+    const int pair = static_cast<int>(cluster_id_x()), n_pairs = static_cast<int>(cluster_count_x());
+    const int n_mt = (p.M + kPairRows - 1) / kPairRows;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kRpStages; ++s) {
+            mbar_init(&full[s], 1);
+            mbar_init(&empty[s], 1);
+        }
+        for (int a = 0; a < 2; ++a) {
+            mbar_init(&acc_full[a], 1);
+            mbar_init(&acc_empty[a], 2 * kGemmEpiWarps);
+        }
+        mbar_init(drain, 1);
+        fence_mbar_init();
+        prefetch_tensormap(&tm_w);
+        prefetch_tensormap(&tm_b);
+    }
+    if (warp == 1) {
+        tmem_alloc_pair(tmem_slot, 512);
+        tmem_relinquish_pair();
+    }
+    ragged_prefix<false>(p, n_mt, kRpBN, false, tile_start);
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync_all();
+    tc_fence_after();
+    const uint32_t tmem_base = *tmem_slot;
+    const int total = tile_start[p.E];
+
+    if (warp == 0) {
+        if (lane == 0) {
+            // ---------------- TMA producer: this CTA's features and half of the rows
+            const uint64_t pol_w = p.weights_once ? policy_evict_first() : policy_evict_normal();
+            const uint64_t pol_x = policy_evict_last();
+            const uint32_t full_lead = mapa_shared(smem_u32(full), 0);
+            constexpr int kElems = I8 ? 128 : 64;  // contraction elements per k-step
+            int stage = 0;
+            uint32_t phase = 0, issued = 0, issued_phase = 0;
+            bool ok = true;
+            for (int item = pair; item < total && ok; item += n_pairs) {
+                const Item it = ragged_item<kRpBN, kRound>(item, tile_start, p);
+                const int half = it.n_mma / 2;
+                const int nbox = (half + kRpBox - 1) / kRpBox;
+                const int b_row = static_cast<int>(it.row0) + static_cast<int>(rank) * half;
+                const int a_row = it.mt * kPairRows + static_cast<int>(rank) * kBM;
+                const uint32_t pair_bytes = 2u * static_cast<uint32_t>(kRgOperand + nbox * kRpBox * kRgRowBytes);
+                for (int kb = 0; kb < p.n_kb; ++kb) {
+                    if (!mbar_wait(&empty[stage], phase ^ 1u, p.timeout)) {
+                        ok = false;
+                        break;
+                    }
+                    uint8_t *sa = smem + stage * 2 * kRgOperand;
+                    const uint32_t bar = full_lead + 8u * static_cast<uint32_t>(stage);
+                    if (rank == 0) mbar_arrive_expect_tx(&full[stage], pair_bytes);
+                    if (A_MN) {
+                        tma_load_3d_pair(sa, &tm_w, bar, a_row, kb * kElems, it.e, pol_w);
+                        tma_load_3d_pair(sa + kRgOperand / 2, &tm_w, bar, a_row + 64, kb * kElems, it.e, pol_w);
+                    } else {
+                        tma_load_3d_pair(sa, &tm_w, bar, kb * kElems, a_row, it.e, pol_w);
+                    }
+                    for (int b = 0; b < nbox; ++b)
+                        tma_load_2d_pair(sa + kRgOperand + b * kRpBox * kRgRowBytes, &tm_b, bar, kb * kElems,
+                                         b_row + b * kRpBox, pol_x);
+                    issued |= 1u << stage;
+                    issued_phase = (issued_phase & ~(1u << stage)) | (phase << stage);
+                    if (++stage == kRpStages) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
+            }
+            // every stage this CTA loaded has been consumed by the pair's MMAs (so its bytes landed)
+            for (int s = 0; s < kRpStages; ++s)
+                if ((issued >> s) & 1u) mbar_wait(&empty[s], (issued_phase >> s) & 1u, p.timeout);
+        }
+    } else if (warp == 1) {
+        if (lane == 0 && rank == 0) {
+            // ---------------- MMA issuer for the pair (leader CTA)
+            int stage = 0;
+            uint32_t phase = 0, uses = 0;
+            bool ok = true;
+            for (int item = pair; item < total && ok; item += n_pairs) {
+                const Item it = ragged_item<kRpBN, kRound>(item, tile_start, p);
+                const uint32_t idesc = idesc_with_n(p.idesc, it.n_mma);
+                for (int kb = 0; kb < p.n_kb && ok; ) {
+                    const int seg_end = min(p.n_kb, kb + p.seg_kb);
+                    if (!mbar_wait_cluster(&acc_empty[uses & 1], ((uses >> 1) & 1u) ^ 1u, p.timeout)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t d = tmem_base + (uses & 1) * 256;
+                    for (bool first = true; kb < seg_end; ++kb, first = false) {
+                        if (!mbar_wait(&full[stage], phase, p.timeout)) {
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after();
+                        const uint32_t sa = smem_u32(smem + stage * 2 * kRgOperand);
+                        const uint64_t da = A_MN ? umma_desc_mn_sw128(sa) : umma_desc_sw128(sa);
+                        const uint64_t db = umma_desc_sw128(sa + kRgOperand);
+#pragma unroll
+                        for (int kk = 0; kk < 4; ++kk) {  // 32 bytes of the contraction per instruction
+                            const uint32_t accum = (!first || kk > 0) ? 1u : 0u;
+                            if (I8) umma_i8_pair(d, da + 2 * kk, db + 2 * kk, idesc, accum);
+                            else umma_bf16_pair(d, da + (A_MN ? 128 : 2) * kk, db + 2 * kk, idesc, accum);
+                        }
+                        umma_commit_pair_both(&empty[stage]);
+                        if (++stage == kRpStages) {
+                            stage = 0;
+                            phase ^= 1u;
+                        }
+                    }
+                    if (!ok) break;
+                    umma_commit_pair_both(&acc_full[uses & 1]);
+                    ++uses;
+                }
+            }
+            umma_commit_pair_self(drain);
+            mbar_wait(drain, 0, p.timeout);
+        }
+    } else {
+        // ---------------- epilogue: two warps per lane quadrant, chunks of 16 rows at 16 sub + 32 i
+        const int q = warp & 3, sub = (warp - 2) / 4;
+        const uint32_t acc_empty_lead = mapa_shared(smem_u32(acc_empty), 0);
+        uint32_t uses = 0;
+        bool ok = true;
+        for (int item = pair; item < total && ok; item += n_pairs) {
+            const Item it = ragged_item<kRpBN, kRound>(item, tile_start, p);
+            uint32_t acc[kRpBN / 32][16];
+            for (int kb = 0; kb < p.n_kb; kb += p.seg_kb, ++uses) {
+                if (!mbar_wait(&acc_full[uses & 1], (uses >> 1) & 1u, p.timeout)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const uint32_t t = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + (uses & 1) * 256;
+                add_segment<I8, kRpBN / 32>(t, sub, 32, it.n_valid, kb == 0, acc);
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_cluster(acc_empty_lead + 8u * (uses & 1));
+            }
+            if (!ok) break;
+            const int m = it.mt * kPairRows + static_cast<int>(rank) * kBM + q * 32 + lane;
+            if (p.out_type == BEAM_MOE_BF16) store_item<I8, BEAM_MOE_BF16, kRpBN / 32>(p, it, sub, m, acc);
+            else if (p.out_type == BEAM_MOE_F16) store_item<I8, BEAM_MOE_F16, kRpBN / 32>(p, it, sub, m, acc);
+            else store_item<I8, BEAM_MOE_F32, kRpBN / 32>(p, it, sub, m, acc);
+        }
+    }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync_all();
+    tc_fence_after();
+    if (warp == 1) tmem_dealloc_pair(tmem_base, 512);
+}
+
+// ---- forward / dgrad with the contraction split over a cluster -------------------------------------
+// For few rows per group, or few items: one product tile of 128 features x up to BN rows per cluster of
+// S = 1, 2, 4 or 8 CTAs; CTA r takes k-steps [r n_kb / S, (r + 1) n_kb / S) and pushes 128 / S features of
+// its partial sums to each CTA of the cluster over distributed shared memory; each CTA adds the S partial
+// sums of its features in rank order (so results do not depend on timing) and stores them.
+template <int BN, int STAGES>
+struct RsplitCfg {
+    static constexpr int kStage = kRgOperand + BN * kRgRowBytes;
+    static constexpr int kRedOff = STAGES * kStage;           // [S][BN][128 / S] fp32 (INT8: int32)
+    static constexpr int kBarOff = kRedOff + BN * kBM * 4;
+    static constexpr int kTileOff = kBarOff + 256;
+    static constexpr int kSmem = 1024 + kTileOff + 4 * (kPmMaxE + 1) + 64;
+    static constexpr int kSlot = BN < 32 ? 32 : BN;
+    static_assert(8 * (2 * STAGES + 4 + 2 + 1) + 4 <= 256, "barrier area");
+    static_assert(kStage % 1024 == 0 && kSmem + 128 <= 232448, "shared memory per CTA");
+};
+constexpr int kRsBox = 16;  // rows per B box
+
+__device__ __forceinline__ void st_cluster_u32(uint32_t addr, uint32_t v) {
+    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+__device__ __forceinline__ void fence_cluster() { asm volatile("fence.acq_rel.cluster;" ::: "memory"); }
+
+// This CTA's features of one item: the S partial sums of two neighbouring features per thread, added in
+// rank order, stored as pairs.  buf: [S][BN][F] in this CTA's shared memory, F = 128 / S.
+template <bool I8, int BN, int TYPE>
+__device__ __forceinline__ void reduce_store(const RaggedParams &p, const Item &it, const float *buf, int S, int F,
+                                             int m0, int tid) {
+    const int pairs = F / 2;
+    for (int idx = tid; idx < it.n_valid * pairs; idx += 32 * kGemmEpiWarps) {
+        const int row = idx / pairs, f = 2 * (idx - row * pairs);
+        const int m = m0 + f;
+        if (m >= p.M) continue;
+        float a = 0.0f, b = 0.0f;
+        if constexpr (I8) {
+            int32_t ia = 0, ib = 0;
+            for (int s = 0; s < S; ++s) {
+                const int2 v = *reinterpret_cast<const int2 *>(buf + (s * BN + row) * F + f);
+                ia += v.x;
+                ib += v.y;
+            }
+            const float rs = __ldg(p.row_scale + it.row0 + row);
+            const float *cs = p.channel_scale + static_cast<int64_t>(it.e) * p.M + m;
+            a = static_cast<float>(ia) * (__ldg(cs) * rs);
+            b = static_cast<float>(ib) * (__ldg(cs + 1) * rs);
+        } else {
+            for (int s = 0; s < S; ++s) {
+                const float2 v = *reinterpret_cast<const float2 *>(buf + (s * BN + row) * F + f);
+                a += v.x;
+                b += v.y;
+            }
+        }
+        const int64_t at = (it.row0 + row) * p.ldo + m;
+        if constexpr (TYPE == BEAM_MOE_F32)
+            *reinterpret_cast<float2 *>(reinterpret_cast<float *>(p.out) + at) = make_float2(a, b);
+        else
+            *reinterpret_cast<uint32_t *>(reinterpret_cast<uint16_t *>(p.out) + at) = pack2<TYPE>(a, b);
+    }
+}
+
+template <bool I8, bool A_MN, int BN, int STAGES>
+__global__ void __launch_bounds__(kRgThreads, 1)
+    ragged_split_kernel(const __grid_constant__ CUtensorMap tm_w,  // weights [E][N][K]
+                        const __grid_constant__ CUtensorMap tm_b,  // rows [R][contraction], kRsBox-row box
+                        const RaggedParams p) {
+    using C = RsplitCfg<BN, STAGES>;
+    constexpr int kChunks = (BN + 31) / 32;
+    extern __shared__ uint8_t gemm_smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(gemm_smem_raw) + 1023) & ~uintptr_t(1023));
+    uint64_t *full = reinterpret_cast<uint64_t *>(smem + C::kBarOff);
+    uint64_t *empty = full + STAGES;
+    uint64_t *acc_full = empty + STAGES;
+    uint64_t *acc_empty = acc_full + 2;
+    uint64_t *red_full = acc_empty + 2;   // all S partial sums of this CTA's features have arrived
+    uint64_t *red_empty = red_full + 1;   // every CTA of the cluster has read its partial sums
+    uint64_t *drain = red_empty + 1;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drain + 1);
+    int *tile_start = reinterpret_cast<int *>(smem + C::kTileOff);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    uint32_t S;
+    asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(S));
+    const uint32_t rank = cluster_ctarank();
+    const int cluster = static_cast<int>(cluster_id_x()), n_clusters = static_cast<int>(cluster_count_x());
+    const int n_mt = (p.M + kBM - 1) / kBM;
+    const int kb0 = static_cast<int>(rank) * p.n_kb / static_cast<int>(S);
+    const int kb1 = (static_cast<int>(rank) + 1) * p.n_kb / static_cast<int>(S);  // S <= n_kb: never empty
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < STAGES; ++s) {
+            mbar_init(&full[s], 1);
+            mbar_init(&empty[s], 1);
+        }
+        for (int a = 0; a < 2; ++a) {
+            mbar_init(&acc_full[a], 1);
+            mbar_init(&acc_empty[a], kGemmEpiWarps);
+        }
+        mbar_init(red_full, kGemmEpiWarps * S);
+        mbar_init(red_empty, kGemmEpiWarps * S);
+        mbar_init(drain, 1);
+        fence_mbar_init();
+        prefetch_tensormap(&tm_w);
+        prefetch_tensormap(&tm_b);
+    }
+    if (warp == 1) {
+        tmem_alloc(tmem_slot, 2 * C::kSlot);
+        tmem_relinquish();
+    }
+    ragged_prefix<false>(p, n_mt, BN, false, tile_start);
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync_all();  // every CTA's barriers are initialised before another one signals them
+    tc_fence_after();
+    const uint32_t tmem_base = *tmem_slot;
+    const int total = tile_start[p.E];
+
+    if (warp == 0) {
+        if (lane == 0) {
+            const uint64_t pol_w = p.weights_once ? policy_evict_first() : policy_evict_normal();
+            const uint64_t pol_x = policy_evict_last();
+            constexpr int kElems = I8 ? 128 : 64;
+            int stage = 0;
+            uint32_t phase = 0, issued = 0, issued_phase = 0;
+            bool ok = true;
+            for (int item = cluster; item < total && ok; item += n_clusters) {
+                const Item it = ragged_item<BN, 16>(item, tile_start, p);
+                const int nbox = it.n_mma / kRsBox;
+                const int a_row = it.mt * kBM;
+                const uint32_t bytes = static_cast<uint32_t>(kRgOperand + nbox * kRsBox * kRgRowBytes);
+                for (int kb = kb0; kb < kb1; ++kb) {
+                    if (!mbar_wait(&empty[stage], phase ^ 1u, p.timeout)) {
+                        ok = false;
+                        break;
+                    }
+                    uint8_t *sa = smem + stage * C::kStage;
+                    mbar_arrive_expect_tx(&full[stage], bytes);
+                    if (A_MN) {
+                        tma_load_3d(sa, &tm_w, &full[stage], a_row, kb * kElems, it.e, pol_w);
+                        tma_load_3d(sa + kRgOperand / 2, &tm_w, &full[stage], a_row + 64, kb * kElems, it.e, pol_w);
+                    } else {
+                        tma_load_3d(sa, &tm_w, &full[stage], kb * kElems, a_row, it.e, pol_w);
+                    }
+                    for (int b = 0; b < nbox; ++b)
+                        tma_load_2d(sa + kRgOperand + b * kRsBox * kRgRowBytes, &tm_b, &full[stage], kb * kElems,
+                                    static_cast<int>(it.row0) + b * kRsBox, pol_x);
+                    issued |= 1u << stage;
+                    issued_phase = (issued_phase & ~(1u << stage)) | (phase << stage);
+                    if (++stage == STAGES) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
+            }
+            for (int s = 0; s < STAGES; ++s)
+                if ((issued >> s) & 1u) mbar_wait(&empty[s], (issued_phase >> s) & 1u, p.timeout);
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            int stage = 0;
+            uint32_t phase = 0, uses = 0;
+            bool ok = true;
+            for (int item = cluster; item < total && ok; item += n_clusters) {
+                const Item it = ragged_item<BN, 16>(item, tile_start, p);
+                const uint32_t idesc = idesc_with_n(p.idesc, it.n_mma);
+                for (int kb = kb0; kb < kb1 && ok;) {
+                    const int seg_end = min(kb1, kb + p.seg_kb);
+                    if (!mbar_wait(&acc_empty[uses & 1], ((uses >> 1) & 1u) ^ 1u, p.timeout)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t d = tmem_base + (uses & 1) * C::kSlot;
+                    for (bool first = true; kb < seg_end; ++kb, first = false) {
+                        if (!mbar_wait(&full[stage], phase, p.timeout)) {
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after();
+                        const uint32_t sa = smem_u32(smem + stage * C::kStage);
+                        const uint64_t da = A_MN ? umma_desc_mn_sw128(sa) : umma_desc_sw128(sa);
+                        const uint64_t db = umma_desc_sw128(sa + kRgOperand);
+#pragma unroll
+                        for (int kk = 0; kk < 4; ++kk) {
+                            const uint32_t accum = (!first || kk > 0) ? 1u : 0u;
+                            if (I8) umma_i8(d, da + 2 * kk, db + 2 * kk, idesc, accum);
+                            else umma_bf16(d, da + (A_MN ? 128 : 2) * kk, db + 2 * kk, idesc, accum);
+                        }
+                        umma_commit(&empty[stage]);
+                        if (++stage == STAGES) {
+                            stage = 0;
+                            phase ^= 1u;
+                        }
+                    }
+                    if (!ok) break;
+                    umma_commit(&acc_full[uses & 1]);
+                    ++uses;
+                }
+            }
+            umma_commit(drain);
+            mbar_wait(drain, 0, p.timeout);
+        }
+    } else {
+        const int q = warp & 3, sub = (warp - 2) / 4;
+        const int F = kBM / static_cast<int>(S);
+        const float *buf = reinterpret_cast<const float *>(smem + C::kRedOff);
+        // this thread's feature q * 32 + lane belongs to CTA `dst`, which keeps it at index f of its F
+        const uint32_t dst = static_cast<uint32_t>(q * 32 + lane) / F;
+        const uint32_t f = static_cast<uint32_t>(q * 32 + lane) % F;
+        const uint32_t push = mapa_shared(smem_u32(buf), dst) + 4u * (rank * BN * F + f);
+        uint32_t uses = 0, n_item = 0;
+        bool ok = true;
+        for (int item = cluster; item < total && ok; item += n_clusters, ++n_item) {
+            const Item it = ragged_item<BN, 16>(item, tile_start, p);
+            uint32_t acc[kChunks][16];
+            for (int kb = kb0; kb < kb1; kb += p.seg_kb, ++uses) {
+                if (!mbar_wait(&acc_full[uses & 1], (uses >> 1) & 1u, p.timeout)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const uint32_t t = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + (uses & 1) * C::kSlot;
+                add_segment<I8, kChunks>(t, sub, 32, it.n_valid, kb == kb0, acc);
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&acc_empty[uses & 1]);
+            }
+            // the last item's partial sums have been read everywhere, then these are pushed
+            ok = ok && mbar_wait_cluster(red_empty, (n_item & 1u) ^ 1u, p.timeout);
+            if (!ok) break;
+#pragma unroll
+            for (int i = 0; i < kChunks; ++i) {
+                const int c = 16 * sub + 32 * i;
+#pragma unroll
+                for (int j = 0; j < 16; ++j)
+                    if (c + j < it.n_valid) st_cluster_u32(push + 4u * static_cast<uint32_t>((c + j) * F), acc[i][j]);
+            }
+            fence_cluster();
+            __syncwarp();
+            if (lane < static_cast<int>(S)) mbar_arrive_cluster(mapa_shared(smem_u32(red_full), lane));
+            if (!mbar_wait_cluster(red_full, n_item & 1u, p.timeout)) {
+                ok = false;
+                break;
+            }
+            const int tid = static_cast<int>(threadIdx.x) - 64;
+            const int m0 = it.mt * kBM + static_cast<int>(rank) * F;
+            if (p.out_type == BEAM_MOE_BF16) reduce_store<I8, BN, BEAM_MOE_BF16>(p, it, buf, S, F, m0, tid);
+            else if (p.out_type == BEAM_MOE_F16) reduce_store<I8, BN, BEAM_MOE_F16>(p, it, buf, S, F, m0, tid);
+            else reduce_store<I8, BN, BEAM_MOE_F32>(p, it, buf, S, F, m0, tid);
+            fence_cluster();
+            __syncwarp();
+            if (lane < static_cast<int>(S)) mbar_arrive_cluster(mapa_shared(smem_u32(red_empty), lane));
+        }
+    }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync_all();  // no CTA leaves while another may still push to it or signal it
+    tc_fence_after();
+    if (warp == 1) tmem_dealloc(tmem_base, 2 * C::kSlot);
+}
+
+// ---- wgrad on CTA pairs ----------------------------------------------------------------------------
+// dw[e][n][k] tiles of 256 x 256: the contraction runs over the group's rows in k-steps of 64, dy^T is the
+// MMA's A (CTA r: columns n 128 r..), x^T its B (CTA r: half of the columns k), both MN-major.  The rows of
+// a group's last k-step that belong to the next group must not enter the sums, and zero times a NaN there
+// would: a helper warp clears them in shared memory.  A staged row is one 128-byte line of each box
+// (swizzling permutes within the line), so rows v.. of a box are the contiguous bytes [128 v, ...), and
+// only the rows up to the next multiple of 16 (one instruction's contraction) are cleared and multiplied.
+//   full[s]   this CTA's loads landed -> helper warp;   ready[s] (leader): both helpers are done -> MMA
+// The epilogue converts 32 rows x 128 bytes per warp into a swizzled staging buffer and stores it with
+// TMA, which clips at N and K; `accumulate` stores with TMA's FP32 add.  Groups without rows store zeros.
+// With `splits` > 1 split s takes its share of each group's k-steps and stores FP32 partial sums at group
+// index s E + e of a [splits E][N][K] workspace, which ragged_join_kernel adds in order.
+constexpr int kRwThreads = 384;  // warp 0 TMA, warp 1 MMA, warp 2 helper, warp 3 idle, warps 4..11 epilogue
+constexpr int kRwStages = 5;
+constexpr int kRwStageOut = 4096;  // one staged output chunk: 32 rows of 128 bytes
+constexpr int kRwOutOff = kRwStages * 2 * kRgOperand;
+constexpr int kRwBarOff = kRwOutOff + kGemmEpiWarps * 2 * kRwStageOut;
+constexpr int kRwTileOff = kRwBarOff + 256;
+constexpr int kRwSmem = 1024 + kRwTileOff + 4 * (kPmMaxE + 1) + 64;
+static_assert(8 * (3 * kRwStages + 2 * 2 + 1) + 4 <= 256, "barrier area");
+static_assert(kRwSmem + 128 <= 232448, "shared memory per CTA (dynamic + the 128 static bytes)");
+
+struct WgradItem {
+    int e, n0, k0, n_mma;  // n_mma: columns of the pair's product (128 or 256)
+    int group;             // group index of the stored tile: split * E + e
+    int64_t row0;
+    int rows;              // rows of this item's share of the group (its first row is row0)
+};
+struct WgradParams {
+    RaggedParams g;  // M = N of the product; n_kb unused
+    int K, n_nt, splits;
+    int accumulate;  // FP32 output: add to it, groups without rows are left alone
+};
+
+__device__ __forceinline__ WgradItem wgrad_item(int item, const int *tile_start, const WgradParams &p) {
+    WgradItem it;
+    it.e = find_group(item, tile_start, p.g.E);
+    int local = item - tile_start[it.e];
+    const int n_mt = (p.g.M + kPairRows - 1) / kPairRows;
+    const int split = local / (n_mt * p.n_nt);
+    local -= split * n_mt * p.n_nt;
+    const int mt = local / p.n_nt;
+    it.n0 = mt * kPairRows;
+    it.k0 = (local - mt * p.n_nt) * 256;
+    it.n_mma = p.K - it.k0 > 128 ? 256 : 128;
+    it.group = split * p.g.E + it.e;
+    const int rows = group_rows(p.g, it.e);
+    const int64_t steps = (rows + 63) / 64;
+    const int r0 = static_cast<int>(steps * split / p.splits) * 64;
+    const int r1 = min(rows, static_cast<int>(steps * (split + 1) / p.splits) * 64);
+    it.row0 = group_begin(p.g, it.e) + r0;
+    it.rows = max(0, r1 - r0);
+    return it;
+}
+
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap *map, const void *src, int c0, int c1, int c2) {
+    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(map), "r"(c0),
+                 "r"(c1), "r"(c2), "r"(smem_u32(src))
+                 : "memory");
+}
+__device__ __forceinline__ void tma_add_3d(const CUtensorMap *map, const void *src, int c0, int c1, int c2) {
+    asm volatile("cp.reduce.async.bulk.tensor.3d.global.shared::cta.add.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(map),
+                 "r"(c0), "r"(c1), "r"(c2), "r"(smem_u32(src))
+                 : "memory");
+}
+__device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void bulk_wait_read() {
+    asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void bulk_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+__device__ __forceinline__ void sts128(uint32_t addr, uint4 v) {
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
+                 : "memory");
+}
+
+// The warp's 32 rows (one per lane) x 128 columns of accumulators: staged 128 bytes per row at a time,
+// swizzled as the tensor map expects, and stored by TMA.  Two staging buffers per warp.
+template <int TYPE>
+__device__ __forceinline__ void wgrad_store(const CUtensorMap *map, const WgradItem &it, int n, int k, int k_end,
+                                            int accumulate, uint32_t stage, const uint8_t *stage_ptr,
+                                            uint32_t &n_out, const uint32_t (&acc)[8][16]) {
+    constexpr int kCols = TYPE == BEAM_MOE_F32 ? 32 : 64;  // columns per 128 bytes
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int b = 0; b < 128 / kCols; ++b) {
+        if (k + b * kCols < k_end) {  // warp-uniform
+            const uint32_t at = (n_out++ & 1) * kRwStageOut;
+            const uint32_t buf = stage + at + lane * 128;
+            if (lane == 0) bulk_wait_read<1>();  // the store before the last one has left this buffer
+            __syncwarp();
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {  // 16 bytes each
+                uint4 v;
+                uint32_t *w = reinterpret_cast<uint32_t *>(&v);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    if constexpr (TYPE == BEAM_MOE_F32) {
+                        const int c = b * 32 + j * 4 + i;
+                        w[i] = acc[c / 16][c % 16];
+                    } else {
+                        const int c = b * 64 + j * 8 + 2 * i;
+                        w[i] = pack2<TYPE>(__uint_as_float(acc[c / 16][c % 16]),
+                                           __uint_as_float(acc[c / 16][c % 16 + 1]));
+                    }
+                }
+                sts128(buf + ((j ^ (lane & 7)) << 4), v);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+                const uint8_t *src = stage_ptr + at;
+                if (accumulate) tma_add_3d(map, src, k + b * kCols, n, it.group);
+                else tma_store_3d(map, src, k + b * kCols, n, it.group);
+                bulk_commit();
+            }
+        }
+    }
+}
+
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kRwThreads, 1)
+    ragged_wgrad_kernel(const __grid_constant__ CUtensorMap tm_dy,  // [R][N], box 64 x 64
+                        const __grid_constant__ CUtensorMap tm_x,   // [R][K], box 64 x 64
+                        const __grid_constant__ CUtensorMap tm_dw,  // [groups][N][K], box 32 rows x 128 bytes
+                        const WgradParams p) {
+    extern __shared__ uint8_t gemm_smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(gemm_smem_raw) + 1023) & ~uintptr_t(1023));
+    uint64_t *full = reinterpret_cast<uint64_t *>(smem + kRwBarOff);
+    uint64_t *empty = full + kRwStages;
+    uint64_t *ready = empty + kRwStages;
+    uint64_t *acc_full = ready + kRwStages;
+    uint64_t *acc_empty = acc_full + 2;
+    uint64_t *drain = acc_empty + 2;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drain + 1);
+    int *tile_start = reinterpret_cast<int *>(smem + kRwTileOff);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_ctarank();
+    const int pair = static_cast<int>(cluster_id_x()), n_pairs = static_cast<int>(cluster_count_x());
+    const int n_mt = (p.g.M + kPairRows - 1) / kPairRows;
+    const long long timeout = p.g.timeout;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kRwStages; ++s) {
+            mbar_init(&full[s], 1);
+            mbar_init(&empty[s], 1);
+            mbar_init(&ready[s], 2);
+        }
+        for (int a = 0; a < 2; ++a) {
+            mbar_init(&acc_full[a], 1);
+            mbar_init(&acc_empty[a], 2 * kGemmEpiWarps);
+        }
+        mbar_init(drain, 1);
+        fence_mbar_init();
+        prefetch_tensormap(&tm_dy);
+        prefetch_tensormap(&tm_x);
+        prefetch_tensormap(&tm_dw);
+    }
+    if (warp == 1) {
+        tmem_alloc_pair(tmem_slot, 512);
+        tmem_relinquish_pair();
+    }
+    ragged_prefix<true>(p.g, n_mt * p.n_nt * p.splits, 1, p.accumulate != 0, tile_start);
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync_all();
+    tc_fence_after();
+    const uint32_t tmem_base = *tmem_slot;
+    const int total = tile_start[p.g.E];
+
+    if (warp == 0) {
+        if (lane == 0) {
+            // ---------------- TMA producer
+            const uint64_t pol = policy_evict_normal();
+            int stage = 0;
+            uint32_t phase = 0, issued = 0, issued_phase = 0;
+            bool ok = true;
+            for (int item = pair; item < total && ok; item += n_pairs) {
+                const WgradItem it = wgrad_item(item, tile_start, p);
+                const int a_col = it.n0 + static_cast<int>(rank) * kBM;
+                const int b_col = it.k0 + static_cast<int>(rank) * (it.n_mma / 2);
+                const int nbox = it.n_mma / 128;  // 64-column boxes of x per CTA
+                const uint32_t bytes = static_cast<uint32_t>(kRgOperand + nbox * (kRgOperand / 2));
+                for (int r = 0; r < it.rows; r += 64) {
+                    if (!mbar_wait(&empty[stage], phase ^ 1u, timeout)) {
+                        ok = false;
+                        break;
+                    }
+                    uint8_t *sa = smem + stage * 2 * kRgOperand;
+                    const int row = static_cast<int>(it.row0) + r;
+                    mbar_arrive_expect_tx(&full[stage], bytes);
+                    tma_load_2d(sa, &tm_dy, &full[stage], a_col, row, pol);
+                    tma_load_2d(sa + kRgOperand / 2, &tm_dy, &full[stage], a_col + 64, row, pol);
+                    for (int b = 0; b < nbox; ++b)
+                        tma_load_2d(sa + kRgOperand + b * (kRgOperand / 2), &tm_x, &full[stage], b_col + 64 * b, row,
+                                    pol);
+                    issued |= 1u << stage;
+                    issued_phase = (issued_phase & ~(1u << stage)) | (phase << stage);
+                    if (++stage == kRwStages) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
+            }
+            for (int s = 0; s < kRwStages; ++s)
+                if ((issued >> s) & 1u) mbar_wait(&empty[s], (issued_phase >> s) & 1u, timeout);
+        }
+    } else if (warp == 1) {
+        if (lane == 0 && rank == 0) {
+            // ---------------- MMA issuer for the pair
+            int stage = 0;
+            uint32_t phase = 0, uses = 0;
+            bool ok = true;
+            for (int item = pair; item < total && ok; item += n_pairs) {
+                const WgradItem it = wgrad_item(item, tile_start, p);
+                const uint32_t idesc = idesc_with_n(p.g.idesc, it.n_mma);
+                const int n_kb = (it.rows + 63) / 64;
+                for (int kb = 0; kb < n_kb && ok;) {
+                    const int seg_end = min(n_kb, kb + p.g.seg_kb);
+                    if (!mbar_wait_cluster(&acc_empty[uses & 1], ((uses >> 1) & 1u) ^ 1u, timeout)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t d = tmem_base + (uses & 1) * 256;
+                    for (bool first = true; kb < seg_end; ++kb, first = false) {
+                        if (!mbar_wait_cluster(&ready[stage], phase, timeout)) {
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after();
+                        const uint32_t sa = smem_u32(smem + stage * 2 * kRgOperand);
+                        const uint64_t da = umma_desc_mn_sw128(sa), db = umma_desc_mn_sw128(sa + kRgOperand);
+                        const int n_mma16 = min(4, (it.rows - kb * 64 + 15) / 16);
+                        for (int kk = 0; kk < n_mma16; ++kk)
+                            umma_bf16_pair(d, da + 128 * kk, db + 128 * kk, idesc, (!first || kk > 0) ? 1u : 0u);
+                        umma_commit_pair_both(&empty[stage]);
+                        if (++stage == kRwStages) {
+                            stage = 0;
+                            phase ^= 1u;
+                        }
+                    }
+                    if (!ok) break;
+                    umma_commit_pair_both(&acc_full[uses & 1]);
+                    ++uses;
+                }
+            }
+            umma_commit_pair_self(drain);
+            mbar_wait(drain, 0, timeout);
+        }
+    } else if (warp == 2) {
+        // ---------------- helper: clears the rows behind the group, passes the stage on to the leader
+        const uint32_t ready_lead = mapa_shared(smem_u32(ready), 0);
+        int stage = 0;
+        uint32_t phase = 0;
+        bool ok = true;
+        for (int item = pair; item < total && ok; item += n_pairs) {
+            const WgradItem it = wgrad_item(item, tile_start, p);
+            for (int r = 0; r < it.rows; r += 64) {
+                if (!mbar_wait(&full[stage], phase, timeout)) {
+                    ok = false;
+                    break;
+                }
+                const int v = it.rows - r;
+                if (v < 64 && (v & 15)) {
+                    const uint32_t sa = smem_u32(smem + stage * 2 * kRgOperand);
+                    const int lines = ((v + 15) & ~15) - v;  // 1..15 lines of 128 bytes per box
+                    const int nbox = 2 + it.n_mma / 128;
+                    for (int i = lane; i < nbox * lines * 8; i += 32) {
+                        const int box = i / (lines * 8), at = i - box * lines * 8;
+                        sts128(sa + box * (kRgOperand / 2) + v * 128 + at * 16, make_uint4(0u, 0u, 0u, 0u));
+                    }
+                    fence_proxy_async_smem();
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive_cluster(ready_lead + 8u * static_cast<uint32_t>(stage));
+                if (++stage == kRwStages) {
+                    stage = 0;
+                    phase ^= 1u;
+                }
+            }
+        }
+    } else if (warp >= 4) {
+        // ---------------- epilogue: lanes = rows n, two warps per quadrant share the product's columns
+        const int q = warp & 3, sub = (warp - 4) / 4;
+        const uint32_t acc_empty_lead = mapa_shared(smem_u32(acc_empty), 0);
+        const uint8_t *stage_ptr = smem + kRwOutOff + (warp - 4) * 2 * kRwStageOut;
+        uint32_t uses = 0, n_out = 0;
+        bool ok = true;
+        for (int item = pair; item < total && ok; item += n_pairs) {
+            const WgradItem it = wgrad_item(item, tile_start, p);
+            const int n_kb = (it.rows + 63) / 64;
+            const int cols = it.n_mma / 2;  // this warp's columns: [cols sub, cols (sub + 1))
+            uint32_t acc[8][16];
+            if (n_kb == 0) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) acc[i][j] = 0u;
+            }
+            for (int kb = 0; kb < n_kb; kb += p.g.seg_kb, ++uses) {
+                if (!mbar_wait(&acc_full[uses & 1], (uses >> 1) & 1u, timeout)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const uint32_t t = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + (uses & 1) * 256 + cols * sub;
+                add_segment<false, 8>(t, 0, 16, cols, kb == 0, acc);
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_cluster(acc_empty_lead + 8u * (uses & 1));
+            }
+            if (!ok) break;
+            const int n = it.n0 + static_cast<int>(rank) * kBM + q * 32;
+            const int k = it.k0 + cols * sub, k_end = min(p.K, k + cols);
+            if (n < p.g.M) {  // warp-uniform
+                const uint32_t stage = smem_u32(stage_ptr);
+                if (p.g.out_type == BEAM_MOE_BF16)
+                    wgrad_store<BEAM_MOE_BF16>(&tm_dw, it, n, k, k_end, 0, stage, stage_ptr, n_out, acc);
+                else if (p.g.out_type == BEAM_MOE_F16)
+                    wgrad_store<BEAM_MOE_F16>(&tm_dw, it, n, k, k_end, 0, stage, stage_ptr, n_out, acc);
+                else
+                    wgrad_store<BEAM_MOE_F32>(&tm_dw, it, n, k, k_end, p.accumulate, stage, stage_ptr, n_out, acc);
+            }
+        }
+        if (lane == 0) bulk_wait_all();
+    }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync_all();
+    tc_fence_after();
+    if (warp == 1) tmem_dealloc_pair(tmem_base, 512);
+}
+
+// dw = (accumulate ? dw : 0) + the FP32 partial sums of `splits` splits in order, n values each.
+template <int TYPE>
+__global__ void __launch_bounds__(256) ragged_join_kernel(const float4 *__restrict__ part, int splits, int64_t n4,
+                                                         int accumulate, void *__restrict__ out,
+                                                         const int64_t *__restrict__ offsets, int E, int64_t R) {
+    const int e = threadIdx.x;  // E <= 256: bad offsets left the partial sums unwritten
+    const bool bad = offsets && e < E && (offsets[e] < 0 || offsets[e + 1] < offsets[e] || offsets[e + 1] > R);
+    if (__syncthreads_or(bad)) return;
+    for (int64_t i = blockIdx.x * 256ll + threadIdx.x; i < n4; i += gridDim.x * 256ll) {
+        float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int s = 0; s < splits; ++s) {
+            const float4 v = __ldg(part + s * n4 + i);
+            a.x += v.x;
+            a.y += v.y;
+            a.z += v.z;
+            a.w += v.w;
+        }
+        if constexpr (TYPE == BEAM_MOE_F32) {
+            float4 *o = reinterpret_cast<float4 *>(out) + i;
+            if (accumulate) {
+                const float4 v = *o;
+                a.x += v.x;
+                a.y += v.y;
+                a.z += v.z;
+                a.w += v.w;
+            }
+            *o = a;
+        } else {
+            reinterpret_cast<uint2 *>(out)[i] = make_uint2(pack2<TYPE>(a.x, a.y), pack2<TYPE>(a.z, a.w));
+        }
+    }
+}
+
+}  // namespace beam

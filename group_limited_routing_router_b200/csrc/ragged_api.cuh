@@ -1,0 +1,483 @@
+// Host side of the grouped products, the INT8 row quantisers and SwiGLU: argument checks, tensor maps,
+// the choice of kernel, launches.  Included by beam_moe.cu, whose device set-up and tensor-map encoder it
+// uses.
+#pragma once
+
+#include "ragged.cuh"
+#include "swiglu.cuh"
+
+namespace beam {
+namespace {
+
+// Split kernels: <BN, stages>.  A few rows per group: 32-row tiles in a 10-deep ring.  More rows but too few
+// tiles for the pairs: 128-row tiles.
+#define RS_FEW_ARGS 32, 10
+#define RS_MID_ARGS 128, 5
+
+struct RaggedDevice {
+    std::once_flag once;
+    int status = BEAM_MOE_OK;
+    int pairs = 0, wgrad_pairs = 0;  // co-resident clusters of 2
+    int clusters[4] = {0, 0, 0, 0};  // split kernels: co-resident clusters of 1, 2, 4, 8 CTAs
+};
+RaggedDevice g_ragged[kMaxDevices];
+
+template <typename F>
+int max_clusters(F *kernel, int threads, int smem, int size, int sms) {
+    cudaLaunchConfig_t lc = {};
+    lc.gridDim = dim3(static_cast<unsigned>(size * (sms / size)), 1, 1);
+    lc.blockDim = dim3(static_cast<unsigned>(threads), 1, 1);
+    lc.dynamicSmemBytes = static_cast<size_t>(smem);
+    cudaLaunchAttribute a[1];
+    a[0].id = cudaLaunchAttributeClusterDimension;
+    a[0].val.clusterDim.x = static_cast<unsigned>(size);
+    a[0].val.clusterDim.y = a[0].val.clusterDim.z = 1;
+    lc.attrs = a;
+    lc.numAttrs = 1;
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, kernel, &lc) != cudaSuccess) return 0;
+    return std::min(n, sms / size);
+}
+template <typename F>
+bool set_smem(F *kernel, int bytes) {
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) == cudaSuccess;
+}
+template <int BN, int ST>
+bool set_split_smem() {
+    constexpr int n = RsplitCfg<BN, ST>::kSmem;
+    return set_smem(ragged_split_kernel<false, false, BN, ST>, n) && set_smem(ragged_split_kernel<false, true, BN, ST>, n) &&
+           set_smem(ragged_split_kernel<true, false, BN, ST>, n);
+}
+
+int init_ragged(int *dev_out) {
+    int rc;
+    if ((rc = init_device(dev_out))) return rc;
+    RaggedDevice &d = g_ragged[*dev_out];
+    const int sms = g_dev[*dev_out].num_sms;
+    std::call_once(d.once, [&]() {
+        bool ok = set_smem(ragged_pair_kernel<false, false>, kRpSmem) && set_smem(ragged_pair_kernel<false, true>, kRpSmem) &&
+                  set_smem(ragged_pair_kernel<true, false>, kRpSmem) && set_smem(ragged_wgrad_kernel, kRwSmem) &&
+                  set_split_smem<RS_FEW_ARGS>() && set_split_smem<RS_MID_ARGS>();
+        if (ok) {
+            d.pairs = max_clusters(ragged_pair_kernel<false, false>, kRgThreads, kRpSmem, 2, sms);
+            d.wgrad_pairs = max_clusters(ragged_wgrad_kernel, kRwThreads, kRwSmem, 2, sms);
+            for (int i = 0; i < 4; ++i)  // both split kernels run one CTA per SM
+                d.clusters[i] = max_clusters(ragged_split_kernel<false, false, RS_MID_ARGS>, kRgThreads,
+                                             RsplitCfg<RS_MID_ARGS>::kSmem, 1 << i, sms);
+            ok = d.pairs > 0 && d.wgrad_pairs > 0 && d.clusters[0] > 0 && d.clusters[1] > 0 && d.clusters[2] > 0 &&
+                 d.clusters[3] > 0;
+        }
+        if (!ok) {
+            cudaGetLastError();
+            d.status = BEAM_MOE_ERR_CUDA;
+        }
+    });
+    return d.status;
+}
+
+// Tensor maps of the operands: rows [rows][width] with a row stride, and weights / results [groups][rows][width].
+bool map_rows(CUtensorMap *m, int esize, const void *base, uint64_t width, uint64_t ld, uint64_t rows, uint32_t box_w,
+              uint32_t box_rows) {
+    const CUtensorMapDataType dt = esize == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+    const cuuint64_t dims[2] = {width, rows};
+    const cuuint64_t strides[1] = {ld * static_cast<uint64_t>(esize)};
+    const cuuint32_t box[2] = {box_w, box_rows};
+    const cuuint32_t estr[2] = {1, 1};
+    return encode_fn()(m, dt, 2, const_cast<void *>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                       CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                       CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+bool map_groups(CUtensorMap *m, CUtensorMapDataType dt, int esize, const void *base, uint64_t width, uint64_t rows,
+                uint64_t groups, uint32_t box_w, uint32_t box_rows) {
+    const cuuint64_t dims[3] = {width, rows, groups};
+    const cuuint64_t strides[2] = {width * esize, width * rows * esize};
+    const cuuint32_t box[3] = {box_w, box_rows, 1};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    return encode_fn()(m, dt, 3, const_cast<void *>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                       CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                       CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+constexpr int64_t kMaxLd = int64_t(1) << 32;
+int type_size(int t) { return t == BEAM_MOE_F32 ? 4 : 2; }
+bool is16(int t) { return t == BEAM_MOE_BF16 || t == BEAM_MOE_F16; }
+bool is_type(int t) { return is16(t) || t == BEAM_MOE_F32; }
+// Width of a matrix: rows of whole 16-byte pieces.
+bool width_ok(int64_t w, int step) { return w >= step && w <= 65536 && w % step == 0; }
+// Row stride: at least the width, rows on 16-byte boundaries.
+bool ld_ok(int64_t ld, int64_t width, int esize) { return ld >= width && ld <= kMaxLd && (ld * esize) % 16 == 0; }
+bool aligned_to(const void *p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+// k-steps per accumulation segment.  A segment's error is the tensor core's truncation, up to 4 instructions
+// per k-step x 2^-23 of the running sum: 16 steps stay below 2^-17, a sixteenth of fp16's half step, and 4
+// steps, for fp32 results, near 2^-20 of a partial sum that is itself a small part of the whole.
+int segment_steps(bool i8, int out_type, int n_kb) {
+    if (i8) return std::max(n_kb, 1);  // INT32 sums are exact
+    return out_type == BEAM_MOE_F32 ? 4 : 16;
+}
+
+uint32_t ragged_idesc(bool i8, int dtype, int M, bool a_mn, bool b_mn) {
+    uint32_t d = static_cast<uint32_t>(M >> 4) << 24;
+    if (i8) return d | (2u << 4) | (1u << 7) | (1u << 10);  // D int32, A and B signed 8-bit
+    const uint32_t f = dtype == BEAM_MOE_BF16 ? 1u : 0u;    // A and B: 0 fp16, 1 bf16; D fp32
+    return d | (1u << 4) | (f << 7) | (f << 10) | ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16);
+}
+
+template <bool I8, bool A_MN, int BN, int ST>
+int launch_split(int S, int clusters, cudaStream_t s, const CUtensorMap &w, const CUtensorMap &b,
+                 const RaggedParams &p) {
+    cudaLaunchConfig_t lc = {};
+    lc.gridDim = dim3(static_cast<unsigned>(S * clusters), 1, 1);
+    lc.blockDim = dim3(kRgThreads, 1, 1);
+    lc.dynamicSmemBytes = RsplitCfg<BN, ST>::kSmem;
+    lc.stream = s;
+    cudaLaunchAttribute a[1];
+    a[0].id = cudaLaunchAttributeClusterDimension;
+    a[0].val.clusterDim.x = static_cast<unsigned>(S);
+    a[0].val.clusterDim.y = a[0].val.clusterDim.z = 1;
+    lc.attrs = a;
+    lc.numAttrs = 1;
+    if (cudaLaunchKernelEx(&lc, ragged_split_kernel<I8, A_MN, BN, ST>, w, b, p) != cudaSuccess) {
+        cudaGetLastError();
+        return BEAM_MOE_ERR_CUDA;
+    }
+    return launch_status();
+}
+template <int BN, int ST>
+int launch_split_any(bool i8, bool a_mn, int S, int clusters, cudaStream_t s, const CUtensorMap &w,
+                     const CUtensorMap &b, const RaggedParams &p) {
+    if (i8) return launch_split<true, false, BN, ST>(S, clusters, s, w, b, p);
+    if (a_mn) return launch_split<false, true, BN, ST>(S, clusters, s, w, b, p);
+    return launch_split<false, false, BN, ST>(S, clusters, s, w, b, p);
+}
+
+// Kernel of a forward / dgrad product from its sizes alone (the counts stay on the device): rows spread
+// over min(E, R) groups.
+struct RaggedPlan {
+    bool pair;
+    bool few;      // split kernels: 32-row tiles
+    int S, log_s;  // split kernels: CTAs per cluster
+    int items;
+};
+RaggedPlan ragged_plan(const RaggedDevice &d, int E, int64_t R, int M, int n_kb) {
+    RaggedPlan P{};
+    const int64_t groups = std::min<int64_t>(E, R);
+    const int64_t mean = (R + groups - 1) / groups;
+    const int64_t pair_items = groups * ((mean + kRpBN - 1) / kRpBN) * ((M + kPairRows - 1) / kPairRows);
+    P.few = mean <= 32;
+    P.pair = !P.few && pair_items >= d.pairs;
+    if (P.pair) return P;
+    const int bn = P.few ? 32 : 128;
+    const int64_t items = groups * ((mean + bn - 1) / bn) * ((M + kBM - 1) / kBM);
+    int64_t best = 0;
+    for (int i = 0; i < 4; ++i) {
+        const int S = 1 << i;
+        if (S > n_kb) break;
+        // rounds over the co-resident clusters x (k-steps per CTA + a fixed cost per item of ~4 steps)
+        const int64_t t = ((items + d.clusters[i] - 1) / d.clusters[i]) * ((n_kb + S - 1) / S + 4);
+        if (i == 0 || t < best) {
+            best = t;
+            P.S = S;
+            P.log_s = i;
+        }
+    }
+    P.items = static_cast<int>(std::min<int64_t>(items, 1 << 30));
+    return P;
+}
+
+struct RaggedCall {
+    bool i8, dgrad;
+    int E;
+    int64_t R;
+    int K, N, dtype, out_type;
+    const void *rows;  // x (forward) or dy (dgrad)
+    int64_t ld_rows;
+    const int64_t *offsets;
+    const void *w;
+    void *out;
+    int64_t ldo;
+    const float *row_scale, *channel_scale;
+};
+
+int ragged_product(const RaggedCall &c, cudaStream_t s) {
+    const int step = c.i8 ? 16 : 8, esize = c.i8 ? 1 : 2;
+    if (c.E < 1 || c.E > kPmMaxE || !width_ok(c.K, step) || !width_ok(c.N, step)) return BEAM_MOE_ERR_INVALID_CONFIG;
+    if (!is_type(c.out_type) || (!c.i8 && (!is16(c.dtype) || (c.out_type != c.dtype && c.out_type != BEAM_MOE_F32))))
+        return BEAM_MOE_ERR_INVALID_ARG;
+    const int width = c.dgrad ? c.N : c.K, M = c.dgrad ? c.K : c.N;  // contraction, output features
+    if (c.R < 0 || c.R > kMaxTokens || !ld_ok(c.ld_rows, width, esize) || !ld_ok(c.ldo, M, type_size(c.out_type)))
+        return BEAM_MOE_ERR_INVALID_ARG;
+    if (c.R == 0) return BEAM_MOE_OK;
+    if (!c.rows || !c.w || !c.out || (!c.offsets && c.E != 1) || (c.i8 && (!c.row_scale || !c.channel_scale)))
+        return BEAM_MOE_ERR_NULL;
+    if (!aligned16(c.rows) || !aligned16(c.w) || !aligned16(c.out) || !aligned_to(c.offsets, 8) ||
+        !aligned_to(c.row_scale, 4) || !aligned_to(c.channel_scale, 4))
+        return BEAM_MOE_ERR_MISALIGNED;
+    int dev, rc;
+    if ((rc = init_ragged(&dev))) return rc;
+    const RaggedDevice &d = g_ragged[dev];
+    if (!encode_fn()) return BEAM_MOE_ERR_CUDA;
+    const int kelems = kRgRowBytes / esize;
+    const int n_kb = (width + kelems - 1) / kelems;
+    const RaggedPlan P = ragged_plan(d, c.E, c.R, M, n_kb);
+    const int bn = P.pair ? kRpBN : (P.few ? 32 : 128);
+    const double mean = static_cast<double>(c.R) / static_cast<double>(std::min<int64_t>(c.E, c.R));
+    RaggedParams p{};
+    p.offsets = c.offsets;
+    p.out = c.out;
+    p.ldo = c.ldo;
+    p.R = c.R;
+    p.E = c.E;
+    p.M = M;
+    p.n_kb = n_kb;
+    p.seg_kb = segment_steps(c.i8, c.out_type, n_kb);
+    p.out_type = c.out_type;
+    p.idesc = ragged_idesc(c.i8, c.dtype, P.pair ? kPairRows : kBM, c.dgrad, false);
+    p.weights_once = mean + 4.0 * std::sqrt(mean) <= bn ? 1 : 0;
+    p.row_scale = c.row_scale;
+    p.channel_scale = c.channel_scale;
+    p.timeout = kDefaultTimeoutCycles;
+    CUtensorMap m_w, m_b;
+    // dgrad's weight tile is 64 features (K, contiguous) by 64 contraction rows (N), two boxes per 128 features
+    if (!map_groups(&m_w, esize == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, esize, c.w,
+                    c.K, c.N, c.E, static_cast<uint32_t>(kelems), c.dgrad ? 64 : kBM) ||
+        !map_rows(&m_b, esize, c.rows, width, c.ld_rows, c.R, static_cast<uint32_t>(kelems), P.pair ? kRpBox : kRsBox))
+        return BEAM_MOE_ERR_CUDA;
+    if (P.pair) {
+        const unsigned grid = static_cast<unsigned>(2 * d.pairs);
+        if (c.i8) ragged_pair_kernel<true, false><<<grid, kRgThreads, kRpSmem, s>>>(m_w, m_b, p);
+        else if (c.dgrad) ragged_pair_kernel<false, true><<<grid, kRgThreads, kRpSmem, s>>>(m_w, m_b, p);
+        else ragged_pair_kernel<false, false><<<grid, kRgThreads, kRpSmem, s>>>(m_w, m_b, p);
+        return launch_status();
+    }
+    // items is an estimate where there are offsets: keep the whole GPU for uneven groups
+    const int clusters = c.offsets ? d.clusters[P.log_s] : std::min(P.items, d.clusters[P.log_s]);
+    return P.few ? launch_split_any<RS_FEW_ARGS>(c.i8, c.dgrad, P.S, clusters, s, m_w, m_b, p)
+                 : launch_split_any<RS_MID_ARGS>(c.i8, c.dgrad, P.S, clusters, s, m_w, m_b, p);
+}
+
+// Splits of wgrad's rows: one where the result's tiles fill the 74 pairs of a 148-SM B200; else enough to
+// fill them, of at least 512 rows of a mean group each.  Pure host arithmetic.
+int wgrad_splits(int E, int64_t R, int K, int N) {
+    const int64_t tiles = static_cast<int64_t>(E) * ((N + 255) / 256) * ((K + 255) / 256);
+    const int64_t by_rows = R / E / 512;
+    return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(74 / tiles, by_rows), 64)));
+}
+size_t wgrad_ws(int E, int64_t R, int K, int N) {
+    const int s = R > 0 ? wgrad_splits(E, R, K, N) : 1;
+    return s > 1 ? static_cast<size_t>(s) * E * N * K * 4 : 0;
+}
+bool wgrad_shape_ok(int E, int K, int N) { return E >= 1 && E <= kPmMaxE && width_ok(K, 8) && width_ok(N, 8); }
+
+// Threads of the SwiGLU kernels: x covers eight columns each, up to 64 wide.
+template <bool BACKWARD>
+int launch_swiglu(int dtype, const SwigluParams &p, cudaStream_t s) {
+    const int vecs = p.I / 8;
+    int bx = 8;
+    while (bx < 64 && bx < vecs) bx *= 2;
+    const int by = 256 / bx;
+    const int64_t gy = (p.R + by - 1) / by;
+    const dim3 grid(static_cast<unsigned>((vecs + bx - 1) / bx), static_cast<unsigned>(std::min<int64_t>(gy, 65535)));
+    const dim3 block(static_cast<unsigned>(bx), static_cast<unsigned>(by));
+    if (dtype == BEAM_MOE_BF16) swiglu_kernel<__nv_bfloat16, BACKWARD><<<grid, block, 0, s>>>(p);
+    else if (dtype == BEAM_MOE_F16) swiglu_kernel<__half, BACKWARD><<<grid, block, 0, s>>>(p);
+    else swiglu_kernel<float, BACKWARD><<<grid, block, 0, s>>>(p);
+    return launch_status();
+}
+
+template <typename T, bool SWIGLU>
+int launch_quant_t(const QuantParams &p, cudaStream_t s) {
+    const int vecs = p.K / 8;
+    if (vecs <= 32 * kQuantCached) {
+        quant_i8_kernel<T, SWIGLU, true><<<static_cast<unsigned>((p.R + 7) / 8), 256, 0, s>>>(p);
+    } else {
+        const int threads = std::min(512, ((vecs + 1) / 2 + 31) / 32 * 32);
+        quant_i8_kernel<T, SWIGLU, false><<<static_cast<unsigned>(p.R), threads, 0, s>>>(p);
+    }
+    return launch_status();
+}
+template <bool SWIGLU>
+int launch_quant(int dtype, const QuantParams &p, cudaStream_t s) {
+    if (dtype == BEAM_MOE_BF16) return launch_quant_t<__nv_bfloat16, SWIGLU>(p, s);
+    if (dtype == BEAM_MOE_F16) return launch_quant_t<__half, SWIGLU>(p, s);
+    return launch_quant_t<float, SWIGLU>(p, s);
+}
+
+int rows_check(int64_t R, int I, int dtype) {
+    if (!width_ok(I, 8)) return BEAM_MOE_ERR_INVALID_CONFIG;
+    if (R < 0 || R > kMaxTokens || !is_type(dtype)) return BEAM_MOE_ERR_INVALID_ARG;
+    return BEAM_MOE_OK;
+}
+
+}  // namespace
+}  // namespace beam
+
+extern "C" {
+
+int beam_moe_grouped_mm(int32_t n_experts, int64_t R, int32_t K, int32_t N, int dtype, const void *x, int64_t ldx,
+                        const int64_t *offsets, const void *w, int out_dtype, void *out, int64_t ldo, void *stream) {
+    return beam::ragged_product({false, false, n_experts, R, K, N, dtype, out_dtype, x, ldx, offsets, w, out, ldo,
+                                 nullptr, nullptr},
+                                static_cast<cudaStream_t>(stream));
+}
+
+int beam_moe_grouped_mm_dgrad(int32_t n_experts, int64_t R, int32_t K, int32_t N, int dtype, const void *dy,
+                              int64_t ldy, const int64_t *offsets, const void *w, int out_dtype, void *dx, int64_t ldx,
+                              void *stream) {
+    return beam::ragged_product({false, true, n_experts, R, K, N, dtype, out_dtype, dy, ldy, offsets, w, dx, ldx,
+                                 nullptr, nullptr},
+                                static_cast<cudaStream_t>(stream));
+}
+
+int beam_moe_grouped_mm_i8(int32_t n_experts, int64_t R, int32_t K, int32_t N, const int8_t *q, const float *row_scale,
+                           const int64_t *offsets, const int8_t *w, const float *channel_scale, int out_dtype,
+                           void *out, int64_t ldo, void *stream) {
+    return beam::ragged_product({true, false, n_experts, R, K, N, BEAM_MOE_BF16, out_dtype, q, K, offsets, w, out, ldo,
+                                 row_scale, channel_scale},
+                                static_cast<cudaStream_t>(stream));
+}
+
+size_t beam_moe_grouped_mm_wgrad_workspace_size(int32_t n_experts, int64_t R, int32_t K, int32_t N) {
+    if (!beam::wgrad_shape_ok(n_experts, K, N) || R < 0 || R > beam::kMaxTokens) return 0;
+    return beam::wgrad_ws(n_experts, R, K, N);
+}
+
+int beam_moe_grouped_mm_wgrad(int32_t n_experts, int64_t R, int32_t K, int32_t N, int dtype, const void *dy,
+                              int64_t ldy, const void *x, int64_t ldx, const int64_t *offsets, int out_dtype, void *dw,
+                              int accumulate, void *ws, size_t ws_bytes, void *stream) {
+    using namespace beam;
+    if (!wgrad_shape_ok(n_experts, K, N)) return BEAM_MOE_ERR_INVALID_CONFIG;
+    if (!is16(dtype) || (out_dtype != dtype && out_dtype != BEAM_MOE_F32) || R < 0 || R > kMaxTokens ||
+        !ld_ok(ldy, N, 2) || !ld_ok(ldx, K, 2) || (accumulate && out_dtype != BEAM_MOE_F32))
+        return BEAM_MOE_ERR_INVALID_ARG;
+    if (!dw) return BEAM_MOE_ERR_NULL;
+    if (!aligned16(dw)) return BEAM_MOE_ERR_MISALIGNED;
+    if (R > 0) {
+        if (!dy || !x || (!offsets && n_experts != 1)) return BEAM_MOE_ERR_NULL;
+        if (!aligned16(dy) || !aligned16(x) || !aligned_to(offsets, 8)) return BEAM_MOE_ERR_MISALIGNED;
+    }
+    const size_t need = wgrad_ws(n_experts, R, K, N);
+    if (need) {
+        if (!ws) return BEAM_MOE_ERR_NULL;
+        if (!aligned16(ws)) return BEAM_MOE_ERR_MISALIGNED;
+        if (ws_bytes < need) return BEAM_MOE_ERR_WORKSPACE_TOO_SMALL;
+    }
+    int dev, rc;
+    if ((rc = init_ragged(&dev))) return rc;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const int64_t n = static_cast<int64_t>(n_experts) * N * K;
+    if (R == 0) {
+        if (!accumulate && cudaMemsetAsync(dw, 0, static_cast<size_t>(n) * type_size(out_dtype), s) != cudaSuccess) {
+            cudaGetLastError();
+            return BEAM_MOE_ERR_CUDA;
+        }
+        return BEAM_MOE_OK;
+    }
+    if (!encode_fn()) return BEAM_MOE_ERR_CUDA;
+    const int splits = wgrad_splits(n_experts, R, K, N);
+    const int store = splits > 1 ? BEAM_MOE_F32 : out_dtype;
+    WgradParams p{};
+    p.g.offsets = offsets;
+    p.g.R = R;
+    p.g.E = n_experts;
+    p.g.M = N;
+    p.g.seg_kb = segment_steps(false, store, 0);
+    p.g.out_type = store;
+    p.g.idesc = ragged_idesc(false, dtype, kPairRows, true, true);
+    p.g.timeout = kDefaultTimeoutCycles;
+    p.K = K;
+    p.n_nt = (K + 255) / 256;
+    p.splits = splits;
+    p.accumulate = splits > 1 ? 0 : (accumulate != 0);
+    const CUtensorMapDataType dt = store == BEAM_MOE_F32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                                                         : (store == BEAM_MOE_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                                                                                  : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16);
+    CUtensorMap m_dy, m_x, m_dw;
+    if (!map_rows(&m_dy, 2, dy, N, ldy, R, 64, 64) || !map_rows(&m_x, 2, x, K, ldx, R, 64, 64) ||
+        !map_groups(&m_dw, dt, type_size(store), splits > 1 ? ws : dw, K, N, static_cast<uint64_t>(splits) * n_experts,
+                    128u / static_cast<uint32_t>(type_size(store)), 32))
+        return BEAM_MOE_ERR_CUDA;
+    ragged_wgrad_kernel<<<static_cast<unsigned>(2 * g_ragged[dev].wgrad_pairs), kRwThreads, kRwSmem, s>>>(m_dy, m_x,
+                                                                                                         m_dw, p);
+    if ((rc = launch_status()) || splits == 1) return rc;
+    const int64_t n4 = n / 4;
+    const unsigned grid = static_cast<unsigned>(std::min<int64_t>((n4 + 255) / 256, 8 * g_dev[dev].num_sms));
+    const float4 *part = static_cast<const float4 *>(ws);
+    if (out_dtype == BEAM_MOE_BF16)
+        ragged_join_kernel<BEAM_MOE_BF16><<<grid, 256, 0, s>>>(part, splits, n4, 0, dw, offsets, n_experts, R);
+    else if (out_dtype == BEAM_MOE_F16)
+        ragged_join_kernel<BEAM_MOE_F16><<<grid, 256, 0, s>>>(part, splits, n4, 0, dw, offsets, n_experts, R);
+    else
+        ragged_join_kernel<BEAM_MOE_F32><<<grid, 256, 0, s>>>(part, splits, n4, accumulate != 0, dw, offsets, n_experts, R);
+    return launch_status();
+}
+
+int beam_moe_quant_i8_rows(int64_t R, int32_t K, int dtype, const void *x, int64_t ldx, int8_t *q, float *scale,
+                           void *stream) {
+    using namespace beam;
+    int rc = rows_check(R, K, dtype);
+    if (rc) return rc;
+    if (!ld_ok(ldx, K, type_size(dtype))) return BEAM_MOE_ERR_INVALID_ARG;
+    if (R == 0) return BEAM_MOE_OK;
+    if (!x || !q || !scale) return BEAM_MOE_ERR_NULL;
+    if (!aligned16(x) || !aligned16(q) || !aligned_to(scale, 4)) return BEAM_MOE_ERR_MISALIGNED;
+    int dev;
+    if ((rc = init_device(&dev))) return rc;
+    return launch_quant<false>(dtype, QuantParams{x, nullptr, ldx, 0, q, scale, R, K}, static_cast<cudaStream_t>(stream));
+}
+
+int beam_moe_swiglu_i8(int64_t R, int32_t I, int dtype, const void *g, int64_t ldg, const void *u, int64_t ldu,
+                       int8_t *q, float *scale, void *stream) {
+    using namespace beam;
+    int rc = rows_check(R, I, dtype);
+    if (rc) return rc;
+    if (!ld_ok(ldg, I, type_size(dtype)) || !ld_ok(ldu, I, type_size(dtype))) return BEAM_MOE_ERR_INVALID_ARG;
+    if (R == 0) return BEAM_MOE_OK;
+    if (!g || !u || !q || !scale) return BEAM_MOE_ERR_NULL;
+    if (!aligned16(g) || !aligned16(u) || !aligned16(q) || !aligned_to(scale, 4)) return BEAM_MOE_ERR_MISALIGNED;
+    int dev;
+    if ((rc = init_device(&dev))) return rc;
+    return launch_quant<true>(dtype, QuantParams{g, u, ldg, ldu, q, scale, R, I}, static_cast<cudaStream_t>(stream));
+}
+
+int beam_moe_swiglu(int64_t R, int32_t I, int dtype, const void *g, int64_t ldg, const void *u, int64_t ldu, void *h,
+                    int64_t ldh, void *stream) {
+    using namespace beam;
+    int rc = rows_check(R, I, dtype);
+    if (rc) return rc;
+    const int es = type_size(dtype);
+    if (!ld_ok(ldg, I, es) || !ld_ok(ldu, I, es) || !ld_ok(ldh, I, es)) return BEAM_MOE_ERR_INVALID_ARG;
+    if (R == 0) return BEAM_MOE_OK;
+    if (!g || !u || !h) return BEAM_MOE_ERR_NULL;
+    if (!aligned16(g) || !aligned16(u) || !aligned16(h)) return BEAM_MOE_ERR_MISALIGNED;
+    int dev;
+    if ((rc = init_device(&dev))) return rc;
+    SwigluParams p{};
+    p.g = g, p.u = u, p.h = h;
+    p.ld_g = ldg, p.ld_u = ldu, p.ld_h = ldh;
+    p.R = R, p.I = I;
+    return launch_swiglu<false>(dtype, p, static_cast<cudaStream_t>(stream));
+}
+
+int beam_moe_swiglu_backward(int64_t R, int32_t I, int dtype, const void *dh, int64_t lddh, const void *g, int64_t ldg,
+                             const void *u, int64_t ldu, void *dg, int64_t lddg, void *du, int64_t lddu, void *stream) {
+    using namespace beam;
+    int rc = rows_check(R, I, dtype);
+    if (rc) return rc;
+    const int es = type_size(dtype);
+    if (!ld_ok(lddh, I, es) || !ld_ok(ldg, I, es) || !ld_ok(ldu, I, es) || !ld_ok(lddg, I, es) || !ld_ok(lddu, I, es))
+        return BEAM_MOE_ERR_INVALID_ARG;
+    if (R == 0) return BEAM_MOE_OK;
+    if (!dh || !g || !u || !dg || !du) return BEAM_MOE_ERR_NULL;
+    if (!aligned16(dh) || !aligned16(g) || !aligned16(u) || !aligned16(dg) || !aligned16(du))
+        return BEAM_MOE_ERR_MISALIGNED;
+    int dev;
+    if ((rc = init_device(&dev))) return rc;
+    SwigluParams p{};
+    p.dh = dh, p.g = g, p.u = u, p.dg = dg, p.du = du;
+    p.ld_dh = lddh, p.ld_g = ldg, p.ld_u = ldu, p.ld_dg = lddg, p.ld_du = lddu;
+    p.R = R, p.I = I;
+    return launch_swiglu<true>(dtype, p, static_cast<cudaStream_t>(stream));
+}
+
+}  // extern "C"

@@ -429,6 +429,98 @@ BEAM_MOE_API int beam_moe_permute_noalloc(const beam_moe_config *cfg, int64_t T,
                                           void *stream);
 
 /*
+ * ---- The experts' steps as operators of their own, with their gradients ------------------------------
+ * For training the experts and for callers that compose their own: matrix products grouped by expert
+ * over ragged rows ("each of the 8 selected experts is a SwiGLU MLP": "Welcome Beam" page, section
+ * "Mixture of Experts"), the same products in INT8, and SwiGLU.  They take the dispatch order of
+ * beam_moe_permute (its offsets, rows gathered by beam_moe_gather_rows).  Common to all of them:
+ *   - Types are given as BEAM_MOE_BF16, BEAM_MOE_F16 or BEAM_MOE_F32.  Sums are FP32 (INT32 for INT8
+ *     operands, exact) and rounded once, to nearest even, when stored.
+ *   - R is the number of rows, 0..2^24.  Widths (K, N, I) are multiples of 8 (INT8 products: 16) in
+ *     8..65536.  Matrices over rows have a row stride ld in elements (at least the width, at most 2^32;
+ *     rows start on 16-byte boundaries); weights and weight gradients are densely packed.
+ *   - offsets [n_experts + 1] int64, device: group e owns rows offsets[e] <= r < offsets[e + 1];
+ *     n_experts is 1..256.  NULL with n_experts = 1: one group of all R rows.  Rows in no group (before
+ *     offsets[0], from offsets[n_experts] on) are neither read nor written.  Offsets that do not ascend
+ *     within [0, R] set BEAM_MOE_ERR_BAD_INDEX in the status word and nothing is written.
+ *   - Results do not depend on timing: the same call gives the same bits.  Outputs may not overlap
+ *     inputs unless a call says so.
+ */
+enum { BEAM_MOE_BF16 = 0, BEAM_MOE_F16 = 1, BEAM_MOE_F32 = 2 };
+
+/*
+ * out[r, n] = sum_k x[r, k] w[e, n, k] for every row r of every group e.
+ *   x [R, K], w [n_experts, N, K] in dtype (BF16 or F16); out [R, N] in out_dtype (dtype or F32)
+ */
+BEAM_MOE_API int beam_moe_grouped_mm(int32_t n_experts, int64_t R, int32_t K, int32_t N, int dtype, const void *x,
+                                     int64_t ldx, const int64_t *offsets, const void *w, int out_dtype, void *out,
+                                     int64_t ldo, void *stream);
+
+/*
+ * Gradient of beam_moe_grouped_mm in its rows: dx[r, k] = sum_n dy[r, n] w[e, n, k].
+ *   dy [R, N], w [n_experts, N, K] in dtype; dx [R, K] in out_dtype (dtype or F32)
+ */
+BEAM_MOE_API int beam_moe_grouped_mm_dgrad(int32_t n_experts, int64_t R, int32_t K, int32_t N, int dtype,
+                                           const void *dy, int64_t ldy, const int64_t *offsets, const void *w,
+                                           int out_dtype, void *dx, int64_t ldx, void *stream);
+
+/*
+ * Gradient of beam_moe_grouped_mm in its weights: dw[e, n, k] = sum over the rows r of group e of
+ * dy[r, n] x[r, k]; zero for a group without rows.  With `accumulate` (out_dtype F32 only) the sums are
+ * added to dw instead; a group without rows then leaves its dw as it is.
+ *   dy [R, N], x [R, K] in dtype; dw [n_experts, N, K] in out_dtype (dtype or F32)
+ *   ws: beam_moe_grouped_mm_wgrad_workspace_size bytes, 16-byte aligned; that size is 0, and ws may be
+ *   NULL, unless few weights meet many rows (the rows are then split and the partial sums added in order).
+ */
+BEAM_MOE_API size_t beam_moe_grouped_mm_wgrad_workspace_size(int32_t n_experts, int64_t R, int32_t K, int32_t N);
+BEAM_MOE_API int beam_moe_grouped_mm_wgrad(int32_t n_experts, int64_t R, int32_t K, int32_t N, int dtype,
+                                           const void *dy, int64_t ldy, const void *x, int64_t ldx,
+                                           const int64_t *offsets, int out_dtype, void *dw, int accumulate, void *ws,
+                                           size_t ws_bytes, void *stream);
+
+/*
+ * Rows to INT8 with one scale each: scale[r] = max_k |x[r, k]| / 127, q[r, k] = x[r, k] / scale[r] to the
+ * nearest integer (ties to even), both quotients in FP32; 0 where scale[r] is 0.  A row that holds an
+ * infinity or a NaN gets that as its scale and codes 0, so that its products are NaN.
+ *   x [R, K] in dtype (any); q [R, K] int8, densely packed; scale [R] fp32
+ */
+BEAM_MOE_API int beam_moe_quant_i8_rows(int64_t R, int32_t K, int dtype, const void *x, int64_t ldx, int8_t *q,
+                                        float *scale, void *stream);
+
+/*
+ * INT8 product with a scale for each row and each output channel of each expert:
+ *   out[r, n] = (sum_k q[r, k] w[e, n, k]) * row_scale[r] * channel_scale[e, n]
+ *   q [R, K] int8 and row_scale [R] fp32 as from beam_moe_quant_i8_rows; w [n_experts, N, K] int8;
+ *   channel_scale [n_experts, N] fp32; out [R, N] in out_dtype (any).  K and N are multiples of 16.
+ */
+BEAM_MOE_API int beam_moe_grouped_mm_i8(int32_t n_experts, int64_t R, int32_t K, int32_t N, const int8_t *q,
+                                        const float *row_scale, const int64_t *offsets, const int8_t *w,
+                                        const float *channel_scale, int out_dtype, void *out, int64_t ldo,
+                                        void *stream);
+
+/*
+ * SwiGLU between the products: h = SiLU(g) * u, elementwise over [R, I] in dtype (any; FP32 arithmetic).
+ * h may be g's or u's own buffer (with the same stride).
+ */
+BEAM_MOE_API int beam_moe_swiglu(int64_t R, int32_t I, int dtype, const void *g, int64_t ldg, const void *u,
+                                 int64_t ldu, void *h, int64_t ldh, void *stream);
+
+/*
+ * Its gradient: dg = dh u sigma(g) (1 + g (1 - sigma(g))), du = dh g sigma(g), all in dtype.  dg and du may
+ * be any two of the inputs' own buffers (each with that input's stride).
+ */
+BEAM_MOE_API int beam_moe_swiglu_backward(int64_t R, int32_t I, int dtype, const void *dh, int64_t lddh,
+                                          const void *g, int64_t ldg, const void *u, int64_t ldu, void *dg,
+                                          int64_t lddg, void *du, int64_t lddu, void *stream);
+
+/*
+ * beam_moe_quant_i8_rows of SiLU(g) * u (kept in FP32) in one pass: the second INT8 product's operand.
+ *   q [R, I] int8, densely packed; scale [R] fp32; neither may overlap g or u
+ */
+BEAM_MOE_API int beam_moe_swiglu_i8(int64_t R, int32_t I, int dtype, const void *g, int64_t ldg, const void *u,
+                                    int64_t ldu, int8_t *q, float *scale, void *stream);
+
+/*
  * Synchronises `stream`, then returns and clears the current device's status word
  * (BEAM_MOE_OK, BEAM_MOE_ERR_DEVICE_TIMEOUT or BEAM_MOE_ERR_BAD_INDEX), or BEAM_MOE_ERR_CUDA.
  */

@@ -27,7 +27,7 @@ def cuda_available() -> bool:
 # checkpoints.  Tests marked `last` run after all others.
 _ORDER = ["test_gpu_route.py", "test_gpu_permute.py", "test_gpu_forward.py", "test_gpu_experts.py", "test_gpu_ep.py",
           "test_gpu_block.py", "test_gpu_dense.py", "test_gpu_fp8.py", "test_gpu_mxfp8.py", "test_gpu_nvfp4.py",
-          "test_gpu_w4a4.py"]
+          "test_gpu_w4a4.py", "test_gpu_ragged.py"]
 
 
 def _rank(item) -> tuple:
