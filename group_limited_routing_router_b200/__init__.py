@@ -639,51 +639,60 @@ TYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 _HALF = (torch.bfloat16, torch.float16)
 
 
-def _rows(t, name: str, dtypes, device=None, shape=None) -> torch.Tensor:
-    """Checks a [rows, width] operand."""
+# (current_stream() builds an object, several times the cost of the whole look-up)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+def _rows(t, name: str, dtypes, device=None, shape=None) -> int:
+    """Checks a [rows, width] operand; its row stride."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor (there is no CPU path)")
     if t.dtype not in dtypes:
         raise TypeError(f"{name} must be one of {[str(d) for d in dtypes]}, got {t.dtype}")
-    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
-        raise ValueError(f"{name} must be a matrix with contiguous rows")
-    if t.shape[0] > 1 and t.stride(0) < t.shape[1]:
-        raise ValueError(f"{name} has overlapping rows (row stride {t.stride(0)} < {t.shape[1]})")
+    size = t.shape
+    if len(size) != 2:
+        raise ValueError(f"{name} must be a matrix, got {tuple(size)}")
+    rows, width = size
+    ld, step = t.stride()
+    if width > 1 and step != 1:
+        raise ValueError(f"{name} must have contiguous rows")
+    if rows <= 1:
+        ld = width
+    elif ld < width:
+        raise ValueError(f"{name} has overlapping rows (row stride {ld} < {width})")
     if device is not None and t.device != device:
         raise ValueError(f"{name} is on {t.device}, expected {device}")
-    if shape is not None and tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    return t
-
-
-def _ld(t: torch.Tensor) -> int:
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+    if shape is not None and size != shape:
+        raise ValueError(f"{name} has shape {tuple(size)}, expected {tuple(shape)}")
+    return ld
 
 
 def _on(t, name: str, dtype, shape, device):
     """_dev, on `device`."""
     _dev(t, name, dtype, shape)
-    if t is not None and t.device != device:
+    if t.device != device:
         raise ValueError(f"{name} is on {t.device}, expected {device}")
     return t
 
 
-def _out_rows(out, name: str, dtypes, default, R: int, width: int, device) -> torch.Tensor:
+def _out_rows(out, name: str, dtype, R: int, width: int, device):
+    """(out, its row stride), allocated where `out` is None."""
     if out is None:
-        return torch.empty(R, width, dtype=default, device=device)
-    return _rows(out, name, dtypes, device, (R, width))
+        return torch.empty((R, width), dtype=dtype, device=device), width
+    return out, _rows(out, name, (dtype,), device, (R, width))
 
 
 def _run(where: str, device, stream, *args, scratch=None):
     """Calls entry point `where` with `args` and the stream, on `device`."""
     if stream is None:
-        handle = torch.cuda.current_stream(device).cuda_stream
+        handle = _raw_stream(device.index)
     else:
         handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
         if scratch is not None:  # allocated here, used there: its memory stays taken until that stream is done
             scratch.record_stream(stream if isinstance(stream, torch.cuda.Stream)
                                   else torch.cuda.ExternalStream(handle, device=device))
-    fn = getattr(lib(), where)
+    fn = getattr(_lib or lib(), where)
     if torch.cuda.current_device() == device.index:
         code = fn(*args, handle)
     else:
@@ -727,29 +736,31 @@ def grouped_mm(x, w, offsets=None, out=None, out_dtype=None, stream=None) -> tor
     x [R, K] and w [E, N, K] bf16 or fp16 (or w [N, K] without offsets: one expert that takes every row);
     offsets [E + 1] int64 on the device (permute()'s); out [R, N] in x's type or fp32.  Rows of no expert
     are not written."""
-    _rows(x, "x", _HALF)
-    w = _weights3(w, "w", x.dtype, x.device)
+    ldx = _rows(x, "x", _HALF)
+    device, dtype = x.device, x.dtype
+    w = _weights3(w, "w", dtype, device)
     (R, K), (E, N, Kw) = x.shape, w.shape
     if K != Kw:
         raise ValueError(f"x has {K} columns, w expects {Kw}")
-    od = _out_type(out, out_dtype, x.dtype)
-    out = _out_rows(out, "out", (od,), od, R, N, x.device)
-    _run("beam_moe_grouped_mm", x.device, stream, E, R, K, N, TYPES[x.dtype], x.data_ptr(), _ld(x),
-         _groups_of(offsets, E, x.device), w.data_ptr(), TYPES[od], out.data_ptr(), _ld(out))
+    od = _out_type(out, out_dtype, dtype)
+    out, ldo = _out_rows(out, "out", od, R, N, device)
+    _run("beam_moe_grouped_mm", device, stream, E, R, K, N, TYPES[dtype], x.data_ptr(), ldx,
+         _groups_of(offsets, E, device), w.data_ptr(), TYPES[od], out.data_ptr(), ldo)
     return out
 
 
 def grouped_mm_dgrad(dy, w, offsets=None, out=None, out_dtype=None, stream=None) -> torch.Tensor:
     """Gradient of grouped_mm in x: dx[r] = w[e]^T dy[r]; dy [R, N], w [E, N, K] (or [N, K]) -> [R, K]."""
-    _rows(dy, "dy", _HALF)
-    w = _weights3(w, "w", dy.dtype, dy.device)
+    ldy = _rows(dy, "dy", _HALF)
+    device, dtype = dy.device, dy.dtype
+    w = _weights3(w, "w", dtype, device)
     (R, N), (E, Nw, K) = dy.shape, w.shape
     if N != Nw:
         raise ValueError(f"dy has {N} columns, w expects {Nw}")
-    od = _out_type(out, out_dtype, dy.dtype)
-    out = _out_rows(out, "out", (od,), od, R, K, dy.device)
-    _run("beam_moe_grouped_mm_dgrad", dy.device, stream, E, R, K, N, TYPES[dy.dtype], dy.data_ptr(), _ld(dy),
-         _groups_of(offsets, E, dy.device), w.data_ptr(), TYPES[od], out.data_ptr(), _ld(out))
+    od = _out_type(out, out_dtype, dtype)
+    out, ldx = _out_rows(out, "out", od, R, K, device)
+    _run("beam_moe_grouped_mm_dgrad", device, stream, E, R, K, N, TYPES[dtype], dy.data_ptr(), ldy,
+         _groups_of(offsets, E, device), w.data_ptr(), TYPES[od], out.data_ptr(), ldx)
     return out
 
 
@@ -758,8 +769,8 @@ def grouped_mm_wgrad(dy, x, offsets=None, out=None, out_dtype=None, accumulate: 
     """Gradient of grouped_mm in w: dw[e] = sum over its rows of dy[r]^T x[r] -> [E, N, K], zeros for an
     expert without rows.  accumulate=True adds to `out` (fp32) instead.  Without offsets: one expert
     (E = 1) that takes every row."""
-    _rows(dy, "dy", _HALF)
-    _rows(x, "x", (dy.dtype,), dy.device)
+    ldy = _rows(dy, "dy", _HALF)
+    ldx = _rows(x, "x", (dy.dtype,), dy.device)
     (R, N), K = dy.shape, x.shape[1]
     if x.shape[0] != R:
         raise ValueError(f"dy has {R} rows, x {x.shape[0]}")
@@ -777,26 +788,30 @@ def grouped_mm_wgrad(dy, x, offsets=None, out=None, out_dtype=None, accumulate: 
             ws = scratch = torch.empty(need, dtype=torch.uint8, device=dy.device)
     else:
         _on(ws, "ws", torch.uint8, None, dy.device)
-    _run("beam_moe_grouped_mm_wgrad", dy.device, stream, E, R, K, N, TYPES[dy.dtype], dy.data_ptr(), _ld(dy),
-         x.data_ptr(), _ld(x), _groups_of(offsets, E, dy.device), TYPES[od], out.data_ptr(), int(bool(accumulate)),
+    _run("beam_moe_grouped_mm_wgrad", dy.device, stream, E, R, K, N, TYPES[dy.dtype], dy.data_ptr(), ldy,
+         x.data_ptr(), ldx, _groups_of(offsets, E, dy.device), TYPES[od], out.data_ptr(), int(bool(accumulate)),
          None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel(), scratch=scratch)
     return out
 
 
 def _codes(q, scale, R: int, K: int, device):
-    q = torch.empty(R, K, dtype=torch.int8, device=device) if q is None else q
-    scale = torch.empty(R, dtype=torch.float32, device=device) if scale is None else scale
-    _on(q, "q", torch.int8, (R, K), device)
-    _on(scale, "scale", torch.float32, (R,), device)
+    if q is None:
+        q = torch.empty((R, K), dtype=torch.int8, device=device)
+    else:
+        _on(q, "q", torch.int8, (R, K), device)
+    if scale is None:
+        scale = torch.empty(R, dtype=torch.float32, device=device)
+    else:
+        _on(scale, "scale", torch.float32, (R,), device)
     return q, scale
 
 
 def quant_i8_rows(x, q=None, scale=None, stream=None):
     """(q [R, K] int8, scale [R] fp32): scale = max|x[r]| / 127, q = x / scale to the nearest integer."""
-    _rows(x, "x", tuple(TYPES))
+    ldx = _rows(x, "x", TYPES)
     R, K = x.shape
     q, scale = _codes(q, scale, R, K, x.device)
-    _run("beam_moe_quant_i8_rows", x.device, stream, R, K, TYPES[x.dtype], x.data_ptr(), _ld(x), q.data_ptr(),
+    _run("beam_moe_quant_i8_rows", x.device, stream, R, K, TYPES[x.dtype], x.data_ptr(), ldx, q.data_ptr(),
          scale.data_ptr())
     return q, scale
 
@@ -820,43 +835,46 @@ def grouped_mm_i8(q, row_scale, w, channel_scale, offsets=None, out=None, out_dt
     _on(row_scale, "row_scale", torch.float32, (R,), device)
     _on(channel_scale, "channel_scale", torch.float32, (E, N), device)
     od = _out_type(out, out_dtype, torch.bfloat16)
-    out = _out_rows(out, "out", (od,), od, R, N, device)
+    out, ldo = _out_rows(out, "out", od, R, N, device)
     _run("beam_moe_grouped_mm_i8", device, stream, E, R, K, N, q.data_ptr(), row_scale.data_ptr(),
-         _groups_of(offsets, E, device), w.data_ptr(), channel_scale.data_ptr(), TYPES[od], out.data_ptr(), _ld(out))
+         _groups_of(offsets, E, device), w.data_ptr(), channel_scale.data_ptr(), TYPES[od], out.data_ptr(), ldo)
     return out
 
 
 def swiglu(g, u, out=None, stream=None) -> torch.Tensor:
     """SiLU(g) * u over [R, I] (bf16, fp16 or fp32); `out` may be g or u."""
-    _rows(g, "g", tuple(TYPES))
-    R, I = g.shape
-    _rows(u, "u", (g.dtype,), g.device, (R, I))
-    out = _out_rows(out, "out", (g.dtype,), g.dtype, R, I, g.device)
-    _run("beam_moe_swiglu", g.device, stream, R, I, TYPES[g.dtype], g.data_ptr(), _ld(g), u.data_ptr(), _ld(u),
-         out.data_ptr(), _ld(out))
+    ldg = _rows(g, "g", TYPES)
+    R, I = size = g.shape
+    device, types = g.device, (g.dtype,)
+    ldu = _rows(u, "u", types, device, size)
+    out, ldo = _out_rows(out, "out", g.dtype, R, I, device)
+    _run("beam_moe_swiglu", device, stream, R, I, TYPES[g.dtype], g.data_ptr(), ldg, u.data_ptr(), ldu,
+         out.data_ptr(), ldo)
     return out
 
 
 def swiglu_backward(dh, g, u, dg=None, du=None, stream=None):
     """Gradients (dg, du) of swiglu; dg and du may be any two of the inputs."""
-    _rows(g, "g", tuple(TYPES))
-    R, I = g.shape
-    _rows(u, "u", (g.dtype,), g.device, (R, I))
-    _rows(dh, "dh", (g.dtype,), g.device, (R, I))
-    dg = _out_rows(dg, "dg", (g.dtype,), g.dtype, R, I, g.device)
-    du = _out_rows(du, "du", (g.dtype,), g.dtype, R, I, g.device)
-    _run("beam_moe_swiglu_backward", g.device, stream, R, I, TYPES[g.dtype], dh.data_ptr(), _ld(dh), g.data_ptr(),
-         _ld(g), u.data_ptr(), _ld(u), dg.data_ptr(), _ld(dg), du.data_ptr(), _ld(du))
+    ldg = _rows(g, "g", TYPES)
+    R, I = size = g.shape
+    device, types = g.device, (g.dtype,)
+    ldu = _rows(u, "u", types, device, size)
+    lddh = _rows(dh, "dh", types, device, size)
+    dg, lddg = _out_rows(dg, "dg", g.dtype, R, I, device)
+    du, lddu = _out_rows(du, "du", g.dtype, R, I, device)
+    _run("beam_moe_swiglu_backward", device, stream, R, I, TYPES[g.dtype], dh.data_ptr(), lddh, g.data_ptr(),
+         ldg, u.data_ptr(), ldu, dg.data_ptr(), lddg, du.data_ptr(), lddu)
     return dg, du
 
 
 def swiglu_i8(g, u, q=None, scale=None, stream=None):
     """quant_i8_rows(SiLU(g) * u) in one pass, the product kept in fp32: (q [R, I] int8, scale [R] fp32)."""
-    _rows(g, "g", tuple(TYPES))
-    R, I = g.shape
-    _rows(u, "u", (g.dtype,), g.device, (R, I))
-    q, scale = _codes(q, scale, R, I, g.device)
-    _run("beam_moe_swiglu_i8", g.device, stream, R, I, TYPES[g.dtype], g.data_ptr(), _ld(g), u.data_ptr(), _ld(u),
+    ldg = _rows(g, "g", TYPES)
+    R, I = size = g.shape
+    device, types = g.device, (g.dtype,)
+    ldu = _rows(u, "u", types, device, size)
+    q, scale = _codes(q, scale, R, I, device)
+    _run("beam_moe_swiglu_i8", device, stream, R, I, TYPES[g.dtype], g.data_ptr(), ldg, u.data_ptr(), ldu,
          q.data_ptr(), scale.data_ptr())
     return q, scale
 

@@ -712,7 +712,13 @@ __global__ void __launch_bounds__(kRgThreads, 1)
 // would: a helper warp clears them in shared memory.  A staged row is one 128-byte line of each box
 // (swizzling permutes within the line), so rows v.. of a box are the contiguous bytes [128 v, ...), and
 // only the rows up to the next multiple of 16 (one instruction's contraction) are cleared and multiplied.
-//   full[s]   this CTA's loads landed -> helper warp;   ready[s] (leader): both helpers are done -> MMA
+//   full[s] (leader)  a whole k-step's loads of both CTAs complete on it directly; for a k-step to clear the
+//                     leader's helper arrives on it once both CTAs have cleared theirs
+//   tail[s]           this CTA's loads of a k-step to clear have landed
+//   cleared[s] (leader)  the peer's helper has cleared its part
+// No thread arrives on the other CTA's barriers for a whole k-step: a remote arrival releases at cluster
+// scope, which waits for the thread's earlier memory operations, and one per k-step held the ring at 700
+// TFLOP/s (with or without the products themselves).
 // The epilogue converts 32 rows x 128 bytes per warp into a swizzled staging buffer and stores it with
 // TMA, which clips at N and K; `accumulate` stores with TMA's FP32 add.  Groups without rows store zeros.
 // With `splits` > 1 split s takes its share of each group's k-steps and stores FP32 partial sums at group
@@ -724,7 +730,7 @@ constexpr int kRwOutOff = kRwStages * 2 * kRgOperand;
 constexpr int kRwBarOff = kRwOutOff + kGemmEpiWarps * 2 * kRwStageOut;
 constexpr int kRwTileOff = kRwBarOff + 256;
 constexpr int kRwSmem = 1024 + kRwTileOff + 4 * (kPmMaxE + 1) + 64;
-static_assert(8 * (3 * kRwStages + 2 * 2 + 1) + 4 <= 256, "barrier area");
+static_assert(8 * (4 * kRwStages + 2 * 2 + 1) + 4 <= 256, "barrier area");
 static_assert(kRwSmem + 128 <= 232448, "shared memory per CTA (dynamic + the 128 static bytes)");
 
 struct WgradItem {
@@ -759,6 +765,9 @@ __device__ __forceinline__ WgradItem wgrad_item(int item, const int *tile_start,
     it.rows = max(0, r1 - r0);
     return it;
 }
+
+// A k-step of v rows of the group (64 or more: whole): whether its last instruction meets rows behind it.
+__device__ __forceinline__ bool needs_clearing(int v) { return v < 64 && (v & 15); }
 
 __device__ __forceinline__ void tma_store_3d(const CUtensorMap *map, const void *src, int c0, int c1, int c2) {
     asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(map), "r"(c0),
@@ -834,10 +843,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kRwThreads, 1)
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(gemm_smem_raw) + 1023) & ~uintptr_t(1023));
     uint64_t *full = reinterpret_cast<uint64_t *>(smem + kRwBarOff);
     uint64_t *empty = full + kRwStages;
-    uint64_t *ready = empty + kRwStages;
-    uint64_t *acc_full = ready + kRwStages;
+    uint64_t *acc_full = empty + kRwStages;
     uint64_t *acc_empty = acc_full + 2;
-    uint64_t *drain = acc_empty + 2;
+    uint64_t *tail = acc_empty + 2;
+    uint64_t *cleared = tail + kRwStages;
+    uint64_t *drain = cleared + kRwStages;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drain + 1);
     int *tile_start = reinterpret_cast<int *>(smem + kRwTileOff);
 
@@ -851,7 +861,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kRwThreads, 1)
         for (int s = 0; s < kRwStages; ++s) {
             mbar_init(&full[s], 1);
             mbar_init(&empty[s], 1);
-            mbar_init(&ready[s], 2);
+            mbar_init(&tail[s], 1);
+            mbar_init(&cleared[s], 1);
         }
         for (int a = 0; a < 2; ++a) {
             mbar_init(&acc_full[a], 1);
@@ -879,6 +890,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kRwThreads, 1)
         if (lane == 0) {
             // ---------------- TMA producer
             const uint64_t pol = policy_evict_normal();
+            const uint32_t full_lead = mapa_shared(smem_u32(full), 0);
+            const uint32_t tail_own = mapa_shared(smem_u32(tail), rank);
             int stage = 0;
             uint32_t phase = 0, issued = 0, issued_phase = 0;
             bool ok = true;
@@ -895,12 +908,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kRwThreads, 1)
                     }
                     uint8_t *sa = smem + stage * 2 * kRgOperand;
                     const int row = static_cast<int>(it.row0) + r;
-                    mbar_arrive_expect_tx(&full[stage], bytes);
-                    tma_load_2d(sa, &tm_dy, &full[stage], a_col, row, pol);
-                    tma_load_2d(sa + kRgOperand / 2, &tm_dy, &full[stage], a_col + 64, row, pol);
+                    uint32_t bar = full_lead + 8u * static_cast<uint32_t>(stage);
+                    if (needs_clearing(it.rows - r)) {
+                        bar = tail_own + 8u * static_cast<uint32_t>(stage);
+                        mbar_arrive_expect_tx(&tail[stage], bytes);
+                    } else if (rank == 0) {
+                        mbar_arrive_expect_tx(&full[stage], 2u * bytes);
+                    }
+                    tma_load_2d_pair(sa, &tm_dy, bar, a_col, row, pol);
+                    tma_load_2d_pair(sa + kRgOperand / 2, &tm_dy, bar, a_col + 64, row, pol);
                     for (int b = 0; b < nbox; ++b)
-                        tma_load_2d(sa + kRgOperand + b * (kRgOperand / 2), &tm_x, &full[stage], b_col + 64 * b, row,
-                                    pol);
+                        tma_load_2d_pair(sa + kRgOperand + b * (kRgOperand / 2), &tm_x, bar, b_col + 64 * b, row, pol);
                     issued |= 1u << stage;
                     issued_phase = (issued_phase & ~(1u << stage)) | (phase << stage);
                     if (++stage == kRwStages) {
@@ -931,7 +949,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kRwThreads, 1)
                     tc_fence_after();
                     const uint32_t d = tmem_base + (uses & 1) * 256;
                     for (bool first = true; kb < seg_end; ++kb, first = false) {
-                        if (!mbar_wait_cluster(&ready[stage], phase, timeout)) {
+                        if (!mbar_wait_cluster(&full[stage], phase, timeout)) {
                             ok = false;
                             break;
                         }
@@ -956,35 +974,34 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kRwThreads, 1)
             mbar_wait(drain, 0, timeout);
         }
     } else if (warp == 2) {
-        // ---------------- helper: clears the rows behind the group, passes the stage on to the leader
-        const uint32_t ready_lead = mapa_shared(smem_u32(ready), 0);
-        int stage = 0;
-        uint32_t phase = 0;
-        bool ok = true;
-        for (int item = pair; item < total && ok; item += n_pairs) {
+        // ---------------- helper: clears the rows behind the group in its last k-step
+        const uint32_t cleared_lead = mapa_shared(smem_u32(cleared), 0);
+        uint32_t steps = 0, phases = 0;  // k-steps up to this item's end; per stage, the phase of tail and cleared
+        for (int item = pair; item < total; item += n_pairs) {
             const WgradItem it = wgrad_item(item, tile_start, p);
-            for (int r = 0; r < it.rows; r += 64) {
-                if (!mbar_wait(&full[stage], phase, timeout)) {
-                    ok = false;
-                    break;
-                }
-                const int v = it.rows - r;
-                if (v < 64 && (v & 15)) {
-                    const uint32_t sa = smem_u32(smem + stage * 2 * kRgOperand);
-                    const int lines = ((v + 15) & ~15) - v;  // 1..15 lines of 128 bytes per box
-                    const int nbox = 2 + it.n_mma / 128;
-                    for (int i = lane; i < nbox * lines * 8; i += 32) {
-                        const int box = i / (lines * 8), at = i - box * lines * 8;
-                        sts128(sa + box * (kRgOperand / 2) + v * 128 + at * 16, make_uint4(0u, 0u, 0u, 0u));
-                    }
-                    fence_proxy_async_smem();
-                }
-                __syncwarp();
-                if (lane == 0) mbar_arrive_cluster(ready_lead + 8u * static_cast<uint32_t>(stage));
-                if (++stage == kRwStages) {
-                    stage = 0;
-                    phase ^= 1u;
-                }
+            if (it.rows == 0) continue;
+            const uint32_t n_kb = static_cast<uint32_t>((it.rows + 63) / 64);
+            steps += n_kb;
+            const int v = it.rows - static_cast<int>(n_kb - 1) * 64;
+            if (!needs_clearing(v)) continue;
+            const uint32_t stage = (steps - 1) % kRwStages;
+            const uint32_t phase = (phases >> stage) & 1u;
+            phases ^= 1u << stage;
+            if (!mbar_wait(&tail[stage], phase, timeout)) break;
+            const uint32_t sa = smem_u32(smem + stage * 2 * kRgOperand);
+            const int lines = ((v + 15) & ~15) - v;  // 1..15 lines of 128 bytes per box
+            const int nbox = 2 + it.n_mma / 128;
+            for (int i = lane; i < nbox * lines * 8; i += 32) {
+                const int box = i / (lines * 8), at = i - box * lines * 8;
+                sts128(sa + box * (kRgOperand / 2) + v * 128 + at * 16, make_uint4(0u, 0u, 0u, 0u));
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (rank != 0) {
+                if (lane == 0) mbar_arrive_cluster(cleared_lead + 8u * stage);
+            } else {
+                if (!mbar_wait_cluster(&cleared[stage], phase, timeout)) break;
+                if (lane == 0) mbar_arrive(&full[stage]);
             }
         }
     } else if (warp >= 4) {
