@@ -86,6 +86,13 @@ __device__ __forceinline__ uint32_t idesc_with_n(uint32_t idesc, int n) {
     return idesc | (static_cast<uint32_t>(n >> 3) << 17);
 }
 
+// Arrives on an accumulator's barrier of either CTA of the pair.  What is handed over is TMEM, ordered by the
+// tcgen05 fences on both sides: no other memory operation has to be performed first, which a release at
+// cluster scope would wait for.
+__device__ __forceinline__ void mbar_arrive_tmem(uint32_t bar_cluster) {
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar_cluster) : "memory");
+}
+
 // mbar_wait whose acquire covers the other CTAs of the cluster (they arrive with release.cluster).
 __device__ __forceinline__ bool mbar_wait_cluster(uint64_t *bar, uint32_t parity, long long timeout) {
     const long long t0 = clock64();
@@ -373,7 +380,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kRgThreads, 1)
                 const uint32_t idesc = idesc_with_n(p.idesc, it.n_mma);
                 for (int kb = 0; kb < p.n_kb && ok; ) {
                     const int seg_end = min(p.n_kb, kb + p.seg_kb);
-                    if (!mbar_wait_cluster(&acc_empty[uses & 1], ((uses >> 1) & 1u) ^ 1u, p.timeout)) {
+                    if (!mbar_wait(&acc_empty[uses & 1], ((uses >> 1) & 1u) ^ 1u, p.timeout)) {
                         ok = false;
                         break;
                     }
@@ -427,7 +434,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kRgThreads, 1)
                 add_segment<I8, kRpBN / 32>(t, sub, 32, it.n_valid, kb == 0, acc);
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive_cluster(acc_empty_lead + 8u * (uses & 1));
+                if (lane == 0) mbar_arrive_tmem(acc_empty_lead + 8u * (uses & 1));
             }
             if (!ok) break;
             const int m = it.mt * kPairRows + static_cast<int>(rank) * kBM + q * 32 + lane;
@@ -942,14 +949,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kRwThreads, 1)
                 const int n_kb = (it.rows + 63) / 64;
                 for (int kb = 0; kb < n_kb && ok;) {
                     const int seg_end = min(n_kb, kb + p.g.seg_kb);
-                    if (!mbar_wait_cluster(&acc_empty[uses & 1], ((uses >> 1) & 1u) ^ 1u, timeout)) {
+                    if (!mbar_wait(&acc_empty[uses & 1], ((uses >> 1) & 1u) ^ 1u, timeout)) {
                         ok = false;
                         break;
                     }
                     tc_fence_after();
                     const uint32_t d = tmem_base + (uses & 1) * 256;
                     for (bool first = true; kb < seg_end; ++kb, first = false) {
-                        if (!mbar_wait_cluster(&full[stage], phase, timeout)) {
+                        if (!mbar_wait(&full[stage], phase, timeout)) {
                             ok = false;
                             break;
                         }
@@ -1032,7 +1039,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kRwThreads, 1)
                 add_segment<false, 8>(t, 0, 16, cols, kb == 0, acc);
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive_cluster(acc_empty_lead + 8u * (uses & 1));
+                if (lane == 0) mbar_arrive_tmem(acc_empty_lead + 8u * (uses & 1));
             }
             if (!ok) break;
             const int n = it.n0 + static_cast<int>(rank) * kBM + q * 32;
