@@ -119,26 +119,56 @@ __device__ __forceinline__ int group_rows(const RaggedParams &p, int e) {
     return static_cast<int>(p.offsets ? p.offsets[e + 1] - p.offsets[e] : p.R);
 }
 
-// Exclusive prefix of the groups' item counts in tile_start[0..E], n_mt items per BN rows of a group
-// (WGRAD: n_mt items per group, `skip_empty` leaving out groups without rows).  Offsets that do not
-// ascend within [0, R] give no items at all.  Contains __syncthreads; E <= 256 <= blockDim.x.
-template <bool WGRAD>
-__device__ __forceinline__ void ragged_prefix(const RaggedParams &p, int n_mt, int BN, bool skip_empty,
-                                              int *tile_start) {
+// Rows of a group's row tiles: as few tiles of at most BN rows as hold them, of even size (a 273-row group in
+// tiles of 256 and 17 would stream its weights a second time for 17 rows).  ROUND is the MMA's step in N.
+template <int BN, int ROUND>
+__device__ __forceinline__ int tile_rows(int rows) {
+    const int n_nt = max(1, (rows + BN - 1) / BN);
+    return ((rows + n_nt - 1) / n_nt + ROUND - 1) / ROUND * ROUND;
+}
+
+// The groups' items: tile_start[i] = items of the groups before place i, tile_start[E] = all.  Each group
+// has n_mt items per row tile (WGRAD: n_mt items, `skip_empty` leaving out groups without rows).  SORT: the
+// places go by falling rows per tile (ties to the lower index), order[i] being the group at place i, so that
+// the items a persistent grid takes side by side take equally long and its last round is the shortest;
+// scratch holds 256 ints.  Offsets that do not ascend within [0, R] give no items at all.  Contains
+// __syncthreads; E <= 256 <= blockDim.x.
+template <int BN, int ROUND, bool WGRAD, bool SORT>
+__device__ __forceinline__ void ragged_items(const RaggedParams &p, int n_mt, bool skip_empty, int *tile_start,
+                                             uint8_t *order, int *scratch) {
     __shared__ int warp_tot[32];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int e = threadIdx.x;
-    int v = 0, bad = 0;
+    int v = 0, bad = 0, rows = 0;
     if (e < p.E) {
         const int64_t lo = p.offsets ? p.offsets[e] : 0, hi = p.offsets ? p.offsets[e + 1] : p.R;
         bad = lo < 0 || hi < lo || hi > p.R;
-        const int64_t rows = bad ? 0 : hi - lo;
+        rows = bad ? 0 : static_cast<int>(hi - lo);
         if (WGRAD) v = (skip_empty && rows == 0) ? 0 : n_mt;
-        else v = n_mt * static_cast<int>((rows + BN - 1) / BN);
+        else v = n_mt * ((rows + BN - 1) / BN);
     }
     bad = __syncthreads_or(bad);
     if (bad) v = 0;
     if (bad && blockIdx.x == 0 && threadIdx.x == 0) set_status(BEAM_MOE_ERR_BAD_INDEX);
+    if constexpr (SORT) {
+        const int key = e < p.E ? (WGRAD ? rows : tile_rows<BN, ROUND>(rows)) : -1;
+        if (e < 256) scratch[e] = key;
+        __syncthreads();
+        int place = 0;
+        if (e < p.E)
+            for (int i = 0; i < p.E; i += 4) {  // entries behind E are -1: never before one of a group
+                const int4 k = *reinterpret_cast<const int4 *>(scratch + i);
+                place += (k.x > key || (k.x == key && i < e)) + (k.y > key || (k.y == key && i + 1 < e)) +
+                         (k.z > key || (k.z == key && i + 2 < e)) + (k.w > key || (k.w == key && i + 3 < e));
+            }
+        __syncthreads();
+        if (e < p.E) {
+            order[place] = static_cast<uint8_t>(e);
+            scratch[place] = v;
+        }
+        __syncthreads();
+        v = e < p.E ? scratch[e] : 0;
+    }
     int incl = v;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
@@ -151,10 +181,11 @@ __device__ __forceinline__ void ragged_prefix(const RaggedParams &p, int n_mt, i
     for (int w = 0; w < warp; ++w) base += warp_tot[w];
     if (e < p.E) tile_start[e] = base + incl - v;
     if (e == p.E - 1) tile_start[p.E] = base + incl;
+    if constexpr (SORT) fence_proxy_async_smem();  // scratch becomes a TMA destination
 }
 
-__device__ __forceinline__ int find_group(int item, const int *tile_start, int E) {
-    int lo = 0, hi = E - 1;  // largest e with tile_start[e] <= item
+__device__ __forceinline__ int find_place(int item, const int *tile_start, int E) {
+    int lo = 0, hi = E - 1;  // largest place with tile_start[place] <= item
     while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
         if (tile_start[mid] <= item) lo = mid;
@@ -163,19 +194,21 @@ __device__ __forceinline__ int find_group(int item, const int *tile_start, int E
     return lo;
 }
 
-// Forward / dgrad item: feature tile mt, row tile nt of group e; ROUND is the MMA's step in N.
+// Forward / dgrad item: feature tile mt, row tile nt of group e.  order: NULL where places are groups.
 template <int BN, int ROUND>
-__device__ __forceinline__ Item ragged_item(int item, const int *tile_start, const RaggedParams &p) {
+__device__ __forceinline__ Item ragged_item(int item, const int *tile_start, const uint8_t *order,
+                                            const RaggedParams &p) {
     Item it;
-    it.e = find_group(item, tile_start, p.E);
+    const int place = find_place(item, tile_start, p.E);
+    it.e = order ? order[place] : place;
     const int rows = group_rows(p, it.e);
-    const int n_nt = (rows + BN - 1) / BN;
-    const int local = item - tile_start[it.e];
+    const int n_nt = (rows + BN - 1) / BN, per = tile_rows<BN, ROUND>(rows);
+    const int local = item - tile_start[place];
     it.mt = local / n_nt;
     it.nt = local - it.mt * n_nt;
-    it.n_valid = min(BN, rows - it.nt * BN);
+    it.n_valid = min(per, rows - it.nt * per);  // > 0: rows > BN (n_nt - 1) >= per (n_nt - 1)
     it.n_mma = (it.n_valid + ROUND - 1) / ROUND * ROUND;
-    it.row0 = group_begin(p, it.e) + static_cast<int64_t>(it.nt) * BN;
+    it.row0 = group_begin(p, it.e) + static_cast<int64_t>(it.nt) * per;
     return it;
 }
 
@@ -221,17 +254,28 @@ __device__ __forceinline__ float ragged_value(const RaggedParams &p, uint32_t ac
 }
 
 // ---- forward / dgrad on CTA pairs ------------------------------------------------------------------
-// The pair engine of gemm_2sm.cuh for one product: a pair computes 256 features x up to 256 rows; CTA r
-// stages features 128 r.. and half of the rows.  Stage = 16 KB + 16 KB, 7 stages, two TMEM slots of 256
-// columns, so that a segment's or an item's epilogue always overlaps the next one's products.
-constexpr int kRpStages = 7;
+// The pair engine of gemm_2sm.cuh for one product.  A pair computes NA x 256 features x up to 256 rows; CTA r
+// stages features 128 r.. of each 256 and half of the rows.
+//   NA = 1: 7 stages of 16 KB + 16 KB, two TMEM slots of 256 columns, so that a segment's or an item's
+//     epilogue always overlaps the next one's products.
+//   NA = 2: 4 stages of 2 x 16 KB + 16 KB.  The staged bytes per product fall by a quarter: with every weight
+//     met by several row tiles NA = 1 is bound by what L2 delivers to the SMs (10.5 TB/s, tensor pipe 67%
+//     busy, bf16 and INT8 alike taking 0.47 us per k-step).  Its one item fills TMEM, so the epilogue packs
+//     the accumulators to 16 bits in registers, hands TMEM back and then stores; fp32 results take NA = 1.
 constexpr int kRpBN = 256;
 constexpr int kRpBox = 32;  // rows per B box
-constexpr int kRpBarOff = kRpStages * 2 * kRgOperand;
-constexpr int kRpTileOff = kRpBarOff + 256;
-constexpr int kRpSmem = 1024 + kRpTileOff + 4 * (kPmMaxE + 1) + 64;
-static_assert(8 * (2 * kRpStages + 2 * 2 + 1) + 4 <= 256, "barrier area");
-static_assert(kRpSmem + 128 <= 232448, "shared memory per CTA (dynamic + the 128 static bytes)");
+template <int NA>
+struct RpairCfg {
+    static constexpr int kStages = NA == 1 ? 7 : 4;
+    static constexpr int kStage = (NA + 1) * kRgOperand;
+    static constexpr int kSlots = NA == 1 ? 2 : 1;
+    static constexpr int kBarOff = kStages * kStage;
+    static constexpr int kTileOff = kBarOff + 256;
+    static constexpr int kOrderOff = kTileOff + 4 * (kPmMaxE + 1);
+    static constexpr int kSmem = 1024 + kOrderOff + kPmMaxE + 60;
+    static_assert(8 * (2 * kStages + 2 * kSlots + 1) + 4 <= 256, "barrier area");
+    static_assert(kSmem + 128 <= 232448, "shared memory per CTA (dynamic + the 128 static bytes)");
+};
 
 // Adds `n_valid` accumulator columns of this warp's share (chunks of 16 at 16 sub + 32 i) to acc.
 template <bool I8, int CHUNKS>
@@ -276,33 +320,89 @@ __device__ __forceinline__ void store_item(const RaggedParams &p, const Item &it
     }
 }
 
-template <bool I8, bool A_MN>
+// NA = 2: this thread's 8 chunks of each of the item's two accumulators, packed to 16 bits: columns 2 j and
+// 2 j + 1 of chunk i of accumulator a in pk[a][i][j].
+template <bool I8, int TYPE>
+__device__ __forceinline__ void pack_item(const RaggedParams &p, const Item &it, uint32_t t, int sub, int m,
+                                          uint32_t (&pk)[2][kRpBN / 32][8]) {
+#pragma unroll
+    for (int a = 0; a < 2; ++a) {
+        const float channel =
+            (I8 && m + a * kPairRows < p.M) ? __ldg(p.channel_scale + static_cast<int64_t>(it.e) * p.M + m + a * kPairRows) : 1.0f;
+#pragma unroll
+        for (int i = 0; i < kRpBN / 32; ++i) {
+            const int c = 16 * sub + 32 * i;
+            if (c < it.n_valid) {  // warp-uniform
+                uint32_t r[16];
+                tmem_ld16(t + a * 256 + c, r);
+                tmem_ld_wait();
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    float row0 = 1.0f, row1 = 1.0f;
+                    if (I8 && c + 2 * j < it.n_valid) row0 = __ldg(p.row_scale + it.row0 + c + 2 * j);
+                    if (I8 && c + 2 * j + 1 < it.n_valid) row1 = __ldg(p.row_scale + it.row0 + c + 2 * j + 1);
+                    pk[a][i][j] = pack2<TYPE>(ragged_value<I8>(p, r[2 * j], channel, row0),
+                                              ragged_value<I8>(p, r[2 * j + 1], channel, row1));
+                }
+            }
+        }
+    }
+}
+// Neighbouring lanes exchange words so that each stores a pair of features of one row.
+__device__ __forceinline__ void store_packed(const RaggedParams &p, const Item &it, int sub, int m,
+                                             const uint32_t (&pk)[2][kRpBN / 32][8]) {
+    const int odd = threadIdx.x & 1;
+    const uint32_t sel = odd ? 0x3276u : 0x5410u;  // odd: (neighbour's high half, own), even: (own, neighbour's low half)
+#pragma unroll
+    for (int a = 0; a < 2; ++a) {
+        const int ma = m + a * kPairRows;
+        uint16_t *o = reinterpret_cast<uint16_t *>(p.out) + (it.row0 + 16 * sub + odd) * p.ldo + (ma & ~1);
+        const int left = ma < p.M ? it.n_valid - 16 * sub - odd : 0;
+#pragma unroll
+        for (int i = 0; i < kRpBN / 32; ++i) {
+            if (16 * sub + 32 * i < it.n_valid) {  // warp-uniform
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const uint32_t got = __shfl_xor_sync(0xffffffffu, pk[a][i][j], 1);
+                    if (32 * i + 2 * j < left) *reinterpret_cast<uint32_t *>(o) = __byte_perm(pk[a][i][j], got, sel);
+                    o += 2 * p.ldo;
+                }
+                o += 16 * p.ldo;
+            }
+        }
+    }
+}
+
+template <bool I8, bool A_MN, int NA>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kRgThreads, 1)
     ragged_pair_kernel(const __grid_constant__ CUtensorMap tm_w,  // weights [E][N][K]
                        const __grid_constant__ CUtensorMap tm_b,  // rows [R][contraction], kRpBox-row box
                        const RaggedParams p) {
+    using C = RpairCfg<NA>;
     constexpr int kRound = I8 ? 32 : 16;
+    constexpr int kStages = C::kStages;
     extern __shared__ uint8_t gemm_smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(gemm_smem_raw) + 1023) & ~uintptr_t(1023));
-    uint64_t *full = reinterpret_cast<uint64_t *>(smem + kRpBarOff);
-    uint64_t *empty = full + kRpStages;
-    uint64_t *acc_full = empty + kRpStages;
-    uint64_t *acc_empty = acc_full + 2;
-    uint64_t *drain = acc_empty + 2;
+    uint64_t *full = reinterpret_cast<uint64_t *>(smem + C::kBarOff);
+    uint64_t *empty = full + kStages;
+    uint64_t *acc_full = empty + kStages;
+    uint64_t *acc_empty = acc_full + C::kSlots;
+    uint64_t *drain = acc_empty + C::kSlots;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drain + 1);
-    int *tile_start = reinterpret_cast<int *>(smem + kRpTileOff);
+    int *tile_start = reinterpret_cast<int *>(smem + C::kTileOff);
+    uint8_t *order = smem + C::kOrderOff;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_ctarank();
     const int pair = static_cast<int>(cluster_id_x()), n_pairs = static_cast<int>(cluster_count_x());
-    const int n_mt = (p.M + kPairRows - 1) / kPairRows;
+    const int n_mt = (p.M + NA * kPairRows - 1) / (NA * kPairRows);
 
     if (threadIdx.x == 0) {
-        for (int s = 0; s < kRpStages; ++s) {
+        for (int s = 0; s < kStages; ++s) {
             mbar_init(&full[s], 1);
             mbar_init(&empty[s], 1);
         }
-        for (int a = 0; a < 2; ++a) {
+        for (int a = 0; a < C::kSlots; ++a) {
             mbar_init(&acc_full[a], 1);
             mbar_init(&acc_empty[a], 2 * kGemmEpiWarps);
         }
@@ -315,7 +415,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kRgThreads, 1)
         tmem_alloc_pair(tmem_slot, 512);
         tmem_relinquish_pair();
     }
-    ragged_prefix<false>(p, n_mt, kRpBN, false, tile_start);
+    ragged_items<kRpBN, kRound, false, true>(p, n_mt, false, tile_start, order, reinterpret_cast<int *>(smem));
     tc_fence_before();
     __syncthreads();
     cluster_sync_all();
@@ -334,39 +434,44 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kRgThreads, 1)
             uint32_t phase = 0, issued = 0, issued_phase = 0;
             bool ok = true;
             for (int item = pair; item < total && ok; item += n_pairs) {
-                const Item it = ragged_item<kRpBN, kRound>(item, tile_start, p);
+                const Item it = ragged_item<kRpBN, kRound>(item, tile_start, order, p);
                 const int half = it.n_mma / 2;
                 const int nbox = (half + kRpBox - 1) / kRpBox;
                 const int b_row = static_cast<int>(it.row0) + static_cast<int>(rank) * half;
-                const int a_row = it.mt * kPairRows + static_cast<int>(rank) * kBM;
-                const uint32_t pair_bytes = 2u * static_cast<uint32_t>(kRgOperand + nbox * kRpBox * kRgRowBytes);
+                const int a_row = it.mt * NA * kPairRows + static_cast<int>(rank) * kBM;
+                const uint32_t pair_bytes = 2u * static_cast<uint32_t>(NA * kRgOperand + nbox * kRpBox * kRgRowBytes);
                 for (int kb = 0; kb < p.n_kb; ++kb) {
                     if (!mbar_wait(&empty[stage], phase ^ 1u, p.timeout)) {
                         ok = false;
                         break;
                     }
-                    uint8_t *sa = smem + stage * 2 * kRgOperand;
+                    uint8_t *sa = smem + stage * C::kStage;
                     const uint32_t bar = full_lead + 8u * static_cast<uint32_t>(stage);
                     if (rank == 0) mbar_arrive_expect_tx(&full[stage], pair_bytes);
-                    if (A_MN) {
-                        tma_load_3d_pair(sa, &tm_w, bar, a_row, kb * kElems, it.e, pol_w);
-                        tma_load_3d_pair(sa + kRgOperand / 2, &tm_w, bar, a_row + 64, kb * kElems, it.e, pol_w);
-                    } else {
-                        tma_load_3d_pair(sa, &tm_w, bar, kb * kElems, a_row, it.e, pol_w);
+#pragma unroll
+                    for (int a = 0; a < NA; ++a) {
+                        uint8_t *dst = sa + a * kRgOperand;
+                        const int row = a_row + a * kPairRows;
+                        if (A_MN) {
+                            tma_load_3d_pair(dst, &tm_w, bar, row, kb * kElems, it.e, pol_w);
+                            tma_load_3d_pair(dst + kRgOperand / 2, &tm_w, bar, row + 64, kb * kElems, it.e, pol_w);
+                        } else {
+                            tma_load_3d_pair(dst, &tm_w, bar, kb * kElems, row, it.e, pol_w);
+                        }
                     }
                     for (int b = 0; b < nbox; ++b)
-                        tma_load_2d_pair(sa + kRgOperand + b * kRpBox * kRgRowBytes, &tm_b, bar, kb * kElems,
+                        tma_load_2d_pair(sa + NA * kRgOperand + b * kRpBox * kRgRowBytes, &tm_b, bar, kb * kElems,
                                          b_row + b * kRpBox, pol_x);
                     issued |= 1u << stage;
                     issued_phase = (issued_phase & ~(1u << stage)) | (phase << stage);
-                    if (++stage == kRpStages) {
+                    if (++stage == kStages) {
                         stage = 0;
                         phase ^= 1u;
                     }
                 }
             }
             // every stage this CTA loaded has been consumed by the pair's MMAs (so its bytes landed)
-            for (int s = 0; s < kRpStages; ++s)
+            for (int s = 0; s < kStages; ++s)
                 if ((issued >> s) & 1u) mbar_wait(&empty[s], (issued_phase >> s) & 1u, p.timeout);
         }
     } else if (warp == 1) {
@@ -376,39 +481,44 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kRgThreads, 1)
             uint32_t phase = 0, uses = 0;
             bool ok = true;
             for (int item = pair; item < total && ok; item += n_pairs) {
-                const Item it = ragged_item<kRpBN, kRound>(item, tile_start, p);
+                const Item it = ragged_item<kRpBN, kRound>(item, tile_start, order, p);
                 const uint32_t idesc = idesc_with_n(p.idesc, it.n_mma);
-                for (int kb = 0; kb < p.n_kb && ok; ) {
-                    const int seg_end = min(p.n_kb, kb + p.seg_kb);
-                    if (!mbar_wait(&acc_empty[uses & 1], ((uses >> 1) & 1u) ^ 1u, p.timeout)) {
+                for (int kb = 0; kb < p.n_kb && ok;) {
+                    const int seg_end = NA == 1 ? min(p.n_kb, kb + p.seg_kb) : p.n_kb;
+                    const uint32_t slot = uses % C::kSlots;
+                    if (!mbar_wait(&acc_empty[slot], ((uses / C::kSlots) & 1u) ^ 1u, p.timeout)) {
                         ok = false;
                         break;
                     }
                     tc_fence_after();
-                    const uint32_t d = tmem_base + (uses & 1) * 256;
+                    const uint32_t d = tmem_base + slot * 256;
                     for (bool first = true; kb < seg_end; ++kb, first = false) {
                         if (!mbar_wait(&full[stage], phase, p.timeout)) {
                             ok = false;
                             break;
                         }
                         tc_fence_after();
-                        const uint32_t sa = smem_u32(smem + stage * 2 * kRgOperand);
-                        const uint64_t da = A_MN ? umma_desc_mn_sw128(sa) : umma_desc_sw128(sa);
-                        const uint64_t db = umma_desc_sw128(sa + kRgOperand);
+                        const uint32_t sa = smem_u32(smem + stage * C::kStage);
+                        const uint64_t db = umma_desc_sw128(sa + NA * kRgOperand);
 #pragma unroll
                         for (int kk = 0; kk < 4; ++kk) {  // 32 bytes of the contraction per instruction
                             const uint32_t accum = (!first || kk > 0) ? 1u : 0u;
-                            if (I8) umma_i8_pair(d, da + 2 * kk, db + 2 * kk, idesc, accum);
-                            else umma_bf16_pair(d, da + (A_MN ? 128 : 2) * kk, db + 2 * kk, idesc, accum);
+#pragma unroll
+                            for (int a = 0; a < NA; ++a) {
+                                const uint32_t at = sa + a * kRgOperand;
+                                const uint64_t da = A_MN ? umma_desc_mn_sw128(at) : umma_desc_sw128(at);
+                                if (I8) umma_i8_pair(d + a * 256, da + 2 * kk, db + 2 * kk, idesc, accum);
+                                else umma_bf16_pair(d + a * 256, da + (A_MN ? 128 : 2) * kk, db + 2 * kk, idesc, accum);
+                            }
                         }
                         umma_commit_pair_both(&empty[stage]);
-                        if (++stage == kRpStages) {
+                        if (++stage == kStages) {
                             stage = 0;
                             phase ^= 1u;
                         }
                     }
                     if (!ok) break;
-                    umma_commit_pair_both(&acc_full[uses & 1]);
+                    umma_commit_pair_both(&acc_full[slot]);
                     ++uses;
                 }
             }
@@ -419,28 +529,42 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kRgThreads, 1)
         // ---------------- epilogue: two warps per lane quadrant, chunks of 16 rows at 16 sub + 32 i
         const int q = warp & 3, sub = (warp - 2) / 4;
         const uint32_t acc_empty_lead = mapa_shared(smem_u32(acc_empty), 0);
+        const uint32_t t0 = tmem_base + (static_cast<uint32_t>(q * 32) << 16);
         uint32_t uses = 0;
         bool ok = true;
         for (int item = pair; item < total && ok; item += n_pairs) {
-            const Item it = ragged_item<kRpBN, kRound>(item, tile_start, p);
-            uint32_t acc[kRpBN / 32][16];
-            for (int kb = 0; kb < p.n_kb; kb += p.seg_kb, ++uses) {
-                if (!mbar_wait(&acc_full[uses & 1], (uses >> 1) & 1u, p.timeout)) {
-                    ok = false;
-                    break;
+            const Item it = ragged_item<kRpBN, kRound>(item, tile_start, order, p);
+            const int m = it.mt * NA * kPairRows + static_cast<int>(rank) * kBM + q * 32 + lane;
+            if constexpr (NA == 1) {
+                uint32_t acc[kRpBN / 32][16];
+                for (int kb = 0; kb < p.n_kb; kb += p.seg_kb, ++uses) {
+                    if (!mbar_wait(&acc_full[uses & 1], (uses >> 1) & 1u, p.timeout)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    add_segment<I8, kRpBN / 32>(t0 + (uses & 1) * 256, sub, 32, it.n_valid, kb == 0, acc);
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_tmem(acc_empty_lead + 8u * (uses & 1));
                 }
+                if (!ok) break;
+                if (p.out_type == BEAM_MOE_BF16) store_item<I8, BEAM_MOE_BF16, kRpBN / 32>(p, it, sub, m, acc);
+                else if (p.out_type == BEAM_MOE_F16) store_item<I8, BEAM_MOE_F16, kRpBN / 32>(p, it, sub, m, acc);
+                else store_item<I8, BEAM_MOE_F32, kRpBN / 32>(p, it, sub, m, acc);
+            } else {
+                uint32_t pk[2][kRpBN / 32][8];
+                ok = mbar_wait(acc_full, uses & 1u, p.timeout);
+                if (!ok) break;
                 tc_fence_after();
-                const uint32_t t = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + (uses & 1) * 256;
-                add_segment<I8, kRpBN / 32>(t, sub, 32, it.n_valid, kb == 0, acc);
+                if (p.out_type == BEAM_MOE_BF16) pack_item<I8, BEAM_MOE_BF16>(p, it, t0, sub, m, pk);
+                else pack_item<I8, BEAM_MOE_F16>(p, it, t0, sub, m, pk);
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive_tmem(acc_empty_lead + 8u * (uses & 1));
+                if (lane == 0) mbar_arrive_tmem(acc_empty_lead);
+                ++uses;
+                store_packed(p, it, sub, m, pk);
             }
-            if (!ok) break;
-            const int m = it.mt * kPairRows + static_cast<int>(rank) * kBM + q * 32 + lane;
-            if (p.out_type == BEAM_MOE_BF16) store_item<I8, BEAM_MOE_BF16, kRpBN / 32>(p, it, sub, m, acc);
-            else if (p.out_type == BEAM_MOE_F16) store_item<I8, BEAM_MOE_F16, kRpBN / 32>(p, it, sub, m, acc);
-            else store_item<I8, BEAM_MOE_F32, kRpBN / 32>(p, it, sub, m, acc);
         }
     }
     __syncwarp();
@@ -559,7 +683,7 @@ __global__ void __launch_bounds__(kRgThreads, 1)
         tmem_alloc(tmem_slot, 2 * C::kSlot);
         tmem_relinquish();
     }
-    ragged_prefix<false>(p, n_mt, BN, false, tile_start);
+    ragged_items<BN, 16, false, false>(p, n_mt, false, tile_start, nullptr, nullptr);
     tc_fence_before();
     __syncthreads();
     cluster_sync_all();  // every CTA's barriers are initialised before another one signals them
@@ -576,7 +700,7 @@ __global__ void __launch_bounds__(kRgThreads, 1)
             uint32_t phase = 0, issued = 0, issued_phase = 0;
             bool ok = true;
             for (int item = cluster; item < total && ok; item += n_clusters) {
-                const Item it = ragged_item<BN, 16>(item, tile_start, p);
+                const Item it = ragged_item<BN, 16>(item, tile_start, nullptr, p);
                 const int nbox = it.n_mma / kRsBox;
                 const int a_row = it.mt * kBM;
                 const uint32_t bytes = static_cast<uint32_t>(kRgOperand + nbox * kRsBox * kRgRowBytes);
@@ -613,7 +737,7 @@ __global__ void __launch_bounds__(kRgThreads, 1)
             uint32_t phase = 0, uses = 0;
             bool ok = true;
             for (int item = cluster; item < total && ok; item += n_clusters) {
-                const Item it = ragged_item<BN, 16>(item, tile_start, p);
+                const Item it = ragged_item<BN, 16>(item, tile_start, nullptr, p);
                 const uint32_t idesc = idesc_with_n(p.idesc, it.n_mma);
                 for (int kb = kb0; kb < kb1 && ok;) {
                     const int seg_end = min(kb1, kb + p.seg_kb);
@@ -663,7 +787,7 @@ __global__ void __launch_bounds__(kRgThreads, 1)
         uint32_t uses = 0, n_item = 0;
         bool ok = true;
         for (int item = cluster; item < total && ok; item += n_clusters, ++n_item) {
-            const Item it = ragged_item<BN, 16>(item, tile_start, p);
+            const Item it = ragged_item<BN, 16>(item, tile_start, nullptr, p);
             uint32_t acc[kChunks][16];
             for (int kb = kb0; kb < kb1; kb += p.seg_kb, ++uses) {
                 if (!mbar_wait(&acc_full[uses & 1], (uses >> 1) & 1u, p.timeout)) {
@@ -736,7 +860,8 @@ constexpr int kRwStageOut = 4096;  // one staged output chunk: 32 rows of 128 by
 constexpr int kRwOutOff = kRwStages * 2 * kRgOperand;
 constexpr int kRwBarOff = kRwOutOff + kGemmEpiWarps * 2 * kRwStageOut;
 constexpr int kRwTileOff = kRwBarOff + 256;
-constexpr int kRwSmem = 1024 + kRwTileOff + 4 * (kPmMaxE + 1) + 64;
+constexpr int kRwOrderOff = kRwTileOff + 4 * (kPmMaxE + 1);
+constexpr int kRwSmem = 1024 + kRwOrderOff + kPmMaxE + 60;
 static_assert(8 * (4 * kRwStages + 2 * 2 + 1) + 4 <= 256, "barrier area");
 static_assert(kRwSmem + 128 <= 232448, "shared memory per CTA (dynamic + the 128 static bytes)");
 
@@ -752,10 +877,12 @@ struct WgradParams {
     int accumulate;  // FP32 output: add to it, groups without rows are left alone
 };
 
-__device__ __forceinline__ WgradItem wgrad_item(int item, const int *tile_start, const WgradParams &p) {
+__device__ __forceinline__ WgradItem wgrad_item(int item, const int *tile_start, const uint8_t *order,
+                                                const WgradParams &p) {
     WgradItem it;
-    it.e = find_group(item, tile_start, p.g.E);
-    int local = item - tile_start[it.e];
+    const int place = find_place(item, tile_start, p.g.E);
+    it.e = order[place];
+    int local = item - tile_start[place];
     const int n_mt = (p.g.M + kPairRows - 1) / kPairRows;
     const int split = local / (n_mt * p.n_nt);
     local -= split * n_mt * p.n_nt;
@@ -857,6 +984,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kRwThreads, 1)
     uint64_t *drain = cleared + kRwStages;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drain + 1);
     int *tile_start = reinterpret_cast<int *>(smem + kRwTileOff);
+    uint8_t *order = smem + kRwOrderOff;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_ctarank();
@@ -885,7 +1013,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kRwThreads, 1)
         tmem_alloc_pair(tmem_slot, 512);
         tmem_relinquish_pair();
     }
-    ragged_prefix<true>(p.g, n_mt * p.n_nt * p.splits, 1, p.accumulate != 0, tile_start);
+    ragged_items<256, 16, true, true>(p.g, n_mt * p.n_nt * p.splits, p.accumulate != 0, tile_start, order,
+                                      reinterpret_cast<int *>(smem));
     tc_fence_before();
     __syncthreads();
     cluster_sync_all();
@@ -903,7 +1032,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kRwThreads, 1)
             uint32_t phase = 0, issued = 0, issued_phase = 0;
             bool ok = true;
             for (int item = pair; item < total && ok; item += n_pairs) {
-                const WgradItem it = wgrad_item(item, tile_start, p);
+                const WgradItem it = wgrad_item(item, tile_start, order, p);
                 const int a_col = it.n0 + static_cast<int>(rank) * kBM;
                 const int b_col = it.k0 + static_cast<int>(rank) * (it.n_mma / 2);
                 const int nbox = it.n_mma / 128;  // 64-column boxes of x per CTA
@@ -944,7 +1073,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kRwThreads, 1)
             uint32_t phase = 0, uses = 0;
             bool ok = true;
             for (int item = pair; item < total && ok; item += n_pairs) {
-                const WgradItem it = wgrad_item(item, tile_start, p);
+                const WgradItem it = wgrad_item(item, tile_start, order, p);
                 const uint32_t idesc = idesc_with_n(p.g.idesc, it.n_mma);
                 const int n_kb = (it.rows + 63) / 64;
                 for (int kb = 0; kb < n_kb && ok;) {
@@ -985,7 +1114,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kRwThreads, 1)
         const uint32_t cleared_lead = mapa_shared(smem_u32(cleared), 0);
         uint32_t steps = 0, phases = 0;  // k-steps up to this item's end; per stage, the phase of tail and cleared
         for (int item = pair; item < total; item += n_pairs) {
-            const WgradItem it = wgrad_item(item, tile_start, p);
+            const WgradItem it = wgrad_item(item, tile_start, order, p);
             if (it.rows == 0) continue;
             const uint32_t n_kb = static_cast<uint32_t>((it.rows + 63) / 64);
             steps += n_kb;
@@ -1019,7 +1148,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kRwThreads, 1)
         uint32_t uses = 0, n_out = 0;
         bool ok = true;
         for (int item = pair; item < total && ok; item += n_pairs) {
-            const WgradItem it = wgrad_item(item, tile_start, p);
+            const WgradItem it = wgrad_item(item, tile_start, order, p);
             const int n_kb = (it.rows + 63) / 64;
             const int cols = it.n_mma / 2;  // this warp's columns: [cols sub, cols (sub + 1))
             uint32_t acc[8][16];

@@ -42,6 +42,12 @@ template <typename F>
 bool set_smem(F *kernel, int bytes) {
     return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) == cudaSuccess;
 }
+template <int NA>
+bool set_pair_smem() {
+    constexpr int n = RpairCfg<NA>::kSmem;
+    return set_smem(ragged_pair_kernel<false, false, NA>, n) && set_smem(ragged_pair_kernel<false, true, NA>, n) &&
+           set_smem(ragged_pair_kernel<true, false, NA>, n);
+}
 template <int BN, int ST>
 bool set_split_smem() {
     constexpr int n = RsplitCfg<BN, ST>::kSmem;
@@ -55,11 +61,11 @@ int init_ragged(int *dev_out) {
     RaggedDevice &d = g_ragged[*dev_out];
     const int sms = g_dev[*dev_out].num_sms;
     std::call_once(d.once, [&]() {
-        bool ok = set_smem(ragged_pair_kernel<false, false>, kRpSmem) && set_smem(ragged_pair_kernel<false, true>, kRpSmem) &&
-                  set_smem(ragged_pair_kernel<true, false>, kRpSmem) && set_smem(ragged_wgrad_kernel, kRwSmem) &&
+        bool ok = set_pair_smem<1>() && set_pair_smem<2>() && set_smem(ragged_wgrad_kernel, kRwSmem) &&
                   set_split_smem<RS_FEW_ARGS>() && set_split_smem<RS_MID_ARGS>();
         if (ok) {
-            d.pairs = max_clusters(ragged_pair_kernel<false, false>, kRgThreads, kRpSmem, 2, sms);
+            // one CTA per SM in all variants
+            d.pairs = max_clusters(ragged_pair_kernel<false, false, 1>, kRgThreads, RpairCfg<1>::kSmem, 2, sms);
             d.wgrad_pairs = max_clusters(ragged_wgrad_kernel, kRwThreads, kRwSmem, 2, sms);
             for (int i = 0; i < 4; ++i)  // both split kernels run one CTA per SM
                 d.clusters[i] = max_clusters(ragged_split_kernel<false, false, RS_MID_ARGS>, kRgThreads,
@@ -151,22 +157,44 @@ int launch_split_any(bool i8, bool a_mn, int S, int clusters, cudaStream_t s, co
     return launch_split<false, false, BN, ST>(S, clusters, s, w, b, p);
 }
 
+template <int NA>
+int launch_pair(bool i8, bool a_mn, int pairs, cudaStream_t s, const CUtensorMap &w, const CUtensorMap &b,
+                const RaggedParams &p) {
+    constexpr int n = RpairCfg<NA>::kSmem;
+    const unsigned grid = static_cast<unsigned>(2 * pairs);
+    if (i8) ragged_pair_kernel<true, false, NA><<<grid, kRgThreads, n, s>>>(w, b, p);
+    else if (a_mn) ragged_pair_kernel<false, true, NA><<<grid, kRgThreads, n, s>>>(w, b, p);
+    else ragged_pair_kernel<false, false, NA><<<grid, kRgThreads, n, s>>>(w, b, p);
+    return launch_status();
+}
+
 // Kernel of a forward / dgrad product from its sizes alone (the counts stay on the device): rows spread
 // over min(E, R) groups.
 struct RaggedPlan {
-    bool pair;
+    int pair;      // 256-feature tiles per CTA pair (1 or 2); 0: the split kernels
     bool few;      // split kernels: 32-row tiles
     int S, log_s;  // split kernels: CTAs per cluster
     int items;
 };
-RaggedPlan ragged_plan(const RaggedDevice &d, int E, int64_t R, int M, int n_kb) {
+RaggedPlan ragged_plan(const RaggedDevice &d, int E, int64_t R, int M, int n_kb, bool out16) {
     RaggedPlan P{};
     const int64_t groups = std::min<int64_t>(E, R);
     const int64_t mean = (R + groups - 1) / groups;
-    const int64_t pair_items = groups * ((mean + kRpBN - 1) / kRpBN) * ((M + kPairRows - 1) / kPairRows);
+    const int64_t row_tiles = groups * ((mean + kRpBN - 1) / kRpBN);
+    const int64_t pair_items = row_tiles * ((M + kPairRows - 1) / kPairRows);
     P.few = mean <= 32;
-    P.pair = !P.few && pair_items >= d.pairs;
-    if (P.pair) return P;
+    if (!P.few && pair_items >= d.pairs) {
+        P.pair = 1;
+        // two feature tiles per pair where groups span several row tiles and the rounds come out shorter: a
+        // k-step costs ~690 cycles with one, ~1060 with two, whose epilogue adds ~2000 per item
+        if (out16 && mean > kRpBN) {
+            const int64_t wide_items = row_tiles * ((M + 2 * kPairRows - 1) / (2 * kPairRows));
+            const int64_t t1 = (pair_items + d.pairs - 1) / d.pairs * n_kb * 690;
+            const int64_t t2 = (wide_items + d.pairs - 1) / d.pairs * (n_kb * int64_t(1060) + 2000);
+            if (t2 < t1) P.pair = 2;
+        }
+        return P;
+    }
     const int bn = P.few ? 32 : 128;
     const int64_t items = groups * ((mean + bn - 1) / bn) * ((M + kBM - 1) / kBM);
     int64_t best = 0;
@@ -219,7 +247,7 @@ int ragged_product(const RaggedCall &c, cudaStream_t s) {
     if (!encode_fn()) return BEAM_MOE_ERR_CUDA;
     const int kelems = kRgRowBytes / esize;
     const int n_kb = (width + kelems - 1) / kelems;
-    const RaggedPlan P = ragged_plan(d, c.E, c.R, M, n_kb);
+    const RaggedPlan P = ragged_plan(d, c.E, c.R, M, n_kb, c.out_type != BEAM_MOE_F32);
     const int bn = P.pair ? kRpBN : (P.few ? 32 : 128);
     const double mean = static_cast<double>(c.R) / static_cast<double>(std::min<int64_t>(c.E, c.R));
     RaggedParams p{};
@@ -243,13 +271,9 @@ int ragged_product(const RaggedCall &c, cudaStream_t s) {
                     c.K, c.N, c.E, static_cast<uint32_t>(kelems), c.dgrad ? 64 : kBM) ||
         !map_rows(&m_b, esize, c.rows, width, c.ld_rows, c.R, static_cast<uint32_t>(kelems), P.pair ? kRpBox : kRsBox))
         return BEAM_MOE_ERR_CUDA;
-    if (P.pair) {
-        const unsigned grid = static_cast<unsigned>(2 * d.pairs);
-        if (c.i8) ragged_pair_kernel<true, false><<<grid, kRgThreads, kRpSmem, s>>>(m_w, m_b, p);
-        else if (c.dgrad) ragged_pair_kernel<false, true><<<grid, kRgThreads, kRpSmem, s>>>(m_w, m_b, p);
-        else ragged_pair_kernel<false, false><<<grid, kRgThreads, kRpSmem, s>>>(m_w, m_b, p);
-        return launch_status();
-    }
+    if (P.pair)
+        return P.pair == 1 ? launch_pair<1>(c.i8, c.dgrad, d.pairs, s, m_w, m_b, p)
+                           : launch_pair<2>(c.i8, c.dgrad, d.pairs, s, m_w, m_b, p);
     // items is an estimate where there are offsets: keep the whole GPU for uneven groups
     const int clusters = c.offsets ? d.clusters[P.log_s] : std::min(P.items, d.clusters[P.log_s]);
     return P.few ? launch_split_any<RS_FEW_ARGS>(c.i8, c.dgrad, P.S, clusters, s, m_w, m_b, p)

@@ -103,7 +103,7 @@ CASES = [  # E, rows, K, N: each kernel, each tile edge
     (1, 1, 64, 64), (1, 1, 8, 8), (1, 7, 72, 136), (2, 5, 64, 128), (3, 40, 320, 192), (4, 333, 512, 384),
     (16, 16, 1024, 512), (16, 1501, 320, 192), (5, 2000, 264, 520), (8, 4096, 640, 1280), (64, 700, 256, 128),
     (256, 300, 128, 256), (256, 2048, 64, 72), (1, 257, 2560, 264), (1, 6000, 128, 248), (2, 3000, 1000, 2056),
-    (37, 12000, 520, 1032),
+    (37, 12000, 520, 1032), (2, 9000, 2040, 520), (2, 9000, 520, 2040),
 ]
 
 
@@ -312,7 +312,8 @@ def i8_operands(g, E, R, K, N):
 
 
 I8_CASES = [(1, 1, 16, 16), (1, 1, 5120, 640), (1, 17, 144, 272), (3, 40, 320, 192), (64, 80, 512, 256),
-            (16, 1501, 320, 192), (1, 300, 2560, 528), (1, 5000, 640, 2560), (8, 9000, 528, 2064)]
+            (16, 1501, 320, 192), (1, 300, 2560, 528), (1, 5000, 640, 2560), (8, 9000, 528, 2064),
+            (2, 9000, 1168, 2032)]
 
 
 @pytest.mark.parametrize("out_dtype", [BF, HF, F32])
