@@ -45,7 +45,6 @@ struct RaggedParams {
     int seg_kb;                  // k-steps per accumulation segment
     int out_type;                // BEAM_MOE_BF16 / F16 / F32
     uint32_t idesc;              // instruction descriptor without N
-    int weights_once;            // 1: each weight tile is read once per call -> L2 evict-first
     const float *row_scale;      // INT8: [R]
     const float *channel_scale;  // INT8: [E, M]
     long long timeout;
@@ -86,10 +85,10 @@ __device__ __forceinline__ uint32_t idesc_with_n(uint32_t idesc, int n) {
     return idesc | (static_cast<uint32_t>(n >> 3) << 17);
 }
 
-// Arrives on an accumulator's barrier of either CTA of the pair.  What is handed over is TMEM, ordered by the
-// tcgen05 fences on both sides: no other memory operation has to be performed first, which a release at
-// cluster scope would wait for.
-__device__ __forceinline__ void mbar_arrive_tmem(uint32_t bar_cluster) {
+// Arrives on a barrier of either CTA of the pair.  What is handed over is TMEM, ordered by the tcgen05 fences
+// on both sides, or this CTA's shared memory after a proxy fence: no other memory operation has to be
+// performed first, which a release at cluster scope would wait for.
+__device__ __forceinline__ void mbar_arrive_async(uint32_t bar_cluster) {
     asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar_cluster) : "memory");
 }
 
@@ -127,48 +126,25 @@ __device__ __forceinline__ int tile_rows(int rows) {
     return ((rows + n_nt - 1) / n_nt + ROUND - 1) / ROUND * ROUND;
 }
 
-// The groups' items: tile_start[i] = items of the groups before place i, tile_start[E] = all.  Each group
-// has n_mt items per row tile (WGRAD: n_mt items, `skip_empty` leaving out groups without rows).  SORT: the
-// places go by falling rows per tile (ties to the lower index), order[i] being the group at place i, so that
-// the items a persistent grid takes side by side take equally long and its last round is the shortest;
-// scratch holds 256 ints.  Offsets that do not ascend within [0, R] give no items at all.  Contains
-// __syncthreads; E <= 256 <= blockDim.x.
-template <int BN, int ROUND, bool WGRAD, bool SORT>
-__device__ __forceinline__ void ragged_items(const RaggedParams &p, int n_mt, bool skip_empty, int *tile_start,
-                                             uint8_t *order, int *scratch) {
+// Exclusive prefix of the groups' item counts in tile_start[0..E]: n_mt items per row tile of a group (WGRAD:
+// n_mt items per group, `skip_empty` leaving out groups without rows).  Offsets that do not ascend within
+// [0, R] give no items at all.  Contains __syncthreads; E <= 256 <= blockDim.x.
+template <int BN, bool WGRAD>
+__device__ __forceinline__ void ragged_prefix(const RaggedParams &p, int n_mt, bool skip_empty, int *tile_start) {
     __shared__ int warp_tot[32];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int e = threadIdx.x;
-    int v = 0, bad = 0, rows = 0;
+    int v = 0, bad = 0;
     if (e < p.E) {
         const int64_t lo = p.offsets ? p.offsets[e] : 0, hi = p.offsets ? p.offsets[e + 1] : p.R;
         bad = lo < 0 || hi < lo || hi > p.R;
-        rows = bad ? 0 : static_cast<int>(hi - lo);
+        const int64_t rows = bad ? 0 : hi - lo;
         if (WGRAD) v = (skip_empty && rows == 0) ? 0 : n_mt;
-        else v = n_mt * ((rows + BN - 1) / BN);
+        else v = n_mt * static_cast<int>((rows + BN - 1) / BN);
     }
     bad = __syncthreads_or(bad);
     if (bad) v = 0;
     if (bad && blockIdx.x == 0 && threadIdx.x == 0) set_status(BEAM_MOE_ERR_BAD_INDEX);
-    if constexpr (SORT) {
-        const int key = e < p.E ? (WGRAD ? rows : tile_rows<BN, ROUND>(rows)) : -1;
-        if (e < 256) scratch[e] = key;
-        __syncthreads();
-        int place = 0;
-        if (e < p.E)
-            for (int i = 0; i < p.E; i += 4) {  // entries behind E are -1: never before one of a group
-                const int4 k = *reinterpret_cast<const int4 *>(scratch + i);
-                place += (k.x > key || (k.x == key && i < e)) + (k.y > key || (k.y == key && i + 1 < e)) +
-                         (k.z > key || (k.z == key && i + 2 < e)) + (k.w > key || (k.w == key && i + 3 < e));
-            }
-        __syncthreads();
-        if (e < p.E) {
-            order[place] = static_cast<uint8_t>(e);
-            scratch[place] = v;
-        }
-        __syncthreads();
-        v = e < p.E ? scratch[e] : 0;
-    }
     int incl = v;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
@@ -181,11 +157,10 @@ __device__ __forceinline__ void ragged_items(const RaggedParams &p, int n_mt, bo
     for (int w = 0; w < warp; ++w) base += warp_tot[w];
     if (e < p.E) tile_start[e] = base + incl - v;
     if (e == p.E - 1) tile_start[p.E] = base + incl;
-    if constexpr (SORT) fence_proxy_async_smem();  // scratch becomes a TMA destination
 }
 
-__device__ __forceinline__ int find_place(int item, const int *tile_start, int E) {
-    int lo = 0, hi = E - 1;  // largest place with tile_start[place] <= item
+__device__ __forceinline__ int find_group(int item, const int *tile_start, int E) {
+    int lo = 0, hi = E - 1;  // largest e with tile_start[e] <= item
     while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
         if (tile_start[mid] <= item) lo = mid;
@@ -194,21 +169,25 @@ __device__ __forceinline__ int find_place(int item, const int *tile_start, int E
     return lo;
 }
 
-// Forward / dgrad item: feature tile mt, row tile nt of group e.  order: NULL where places are groups.
+// Forward / dgrad item: feature tile mt, row tile of group e.
+struct RaggedItem {
+    int e, mt, n_valid, n_mma;
+    int once;  // the group has one row tile, so its weights are read once: L2 evict-first
+    int64_t row0;
+};
 template <int BN, int ROUND>
-__device__ __forceinline__ Item ragged_item(int item, const int *tile_start, const uint8_t *order,
-                                            const RaggedParams &p) {
-    Item it;
-    const int place = find_place(item, tile_start, p.E);
-    it.e = order ? order[place] : place;
+__device__ __forceinline__ RaggedItem ragged_item(int item, const int *tile_start, const RaggedParams &p) {
+    RaggedItem it;
+    it.e = find_group(item, tile_start, p.E);
     const int rows = group_rows(p, it.e);
     const int n_nt = (rows + BN - 1) / BN, per = tile_rows<BN, ROUND>(rows);
-    const int local = item - tile_start[place];
+    const int local = item - tile_start[it.e];
     it.mt = local / n_nt;
-    it.nt = local - it.mt * n_nt;
-    it.n_valid = min(per, rows - it.nt * per);  // > 0: rows > BN (n_nt - 1) >= per (n_nt - 1)
+    const int nt = local - it.mt * n_nt;
+    it.n_valid = min(per, rows - nt * per);  // > 0: rows > BN (n_nt - 1) >= per (n_nt - 1)
     it.n_mma = (it.n_valid + ROUND - 1) / ROUND * ROUND;
-    it.row0 = group_begin(p, it.e) + static_cast<int64_t>(it.nt) * per;
+    it.once = n_nt == 1;
+    it.row0 = group_begin(p, it.e) + static_cast<int64_t>(nt) * per;
     return it;
 }
 
@@ -228,7 +207,7 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
 // Feature m (this lane; M and the lane pairing make m and m ^ 1 valid together) of rows c..c+15.  16-bit
 // outputs: neighbouring lanes exchange every other row so that each stores a pair of features.
 template <int TYPE>
-__device__ __forceinline__ void store_cols(const RaggedParams &p, const Item &it, int c, int m, const float (&v)[16]) {
+__device__ __forceinline__ void store_cols(const RaggedParams &p, const RaggedItem &it, int c, int m, const float (&v)[16]) {
     const int lane = threadIdx.x & 31;
     if constexpr (TYPE == BEAM_MOE_F32) {
         float *o = reinterpret_cast<float *>(p.out) + (it.row0 + c) * p.ldo + m;
@@ -261,7 +240,8 @@ __device__ __forceinline__ float ragged_value(const RaggedParams &p, uint32_t ac
 //   NA = 2: 4 stages of 2 x 16 KB + 16 KB.  The staged bytes per product fall by a quarter: with every weight
 //     met by several row tiles NA = 1 is bound by what L2 delivers to the SMs (10.5 TB/s, tensor pipe 67%
 //     busy, bf16 and INT8 alike taking 0.47 us per k-step).  Its one item fills TMEM, so the epilogue packs
-//     the accumulators to 16 bits in registers, hands TMEM back and then stores; fp32 results take NA = 1.
+//     the accumulators to 16 bits in registers, hands TMEM back and then stores; fp32 results (of INT8 only:
+//     16-bit operands keep their short segments there) are stored chunk by chunk before TMEM goes back.
 constexpr int kRpBN = 256;
 constexpr int kRpBox = 32;  // rows per B box
 template <int NA>
@@ -271,8 +251,7 @@ struct RpairCfg {
     static constexpr int kSlots = NA == 1 ? 2 : 1;
     static constexpr int kBarOff = kStages * kStage;
     static constexpr int kTileOff = kBarOff + 256;
-    static constexpr int kOrderOff = kTileOff + 4 * (kPmMaxE + 1);
-    static constexpr int kSmem = 1024 + kOrderOff + kPmMaxE + 60;
+    static constexpr int kSmem = 1024 + kTileOff + 4 * (kPmMaxE + 1) + 64;
     static_assert(8 * (2 * kStages + 2 * kSlots + 1) + 4 <= 256, "barrier area");
     static_assert(kSmem + 128 <= 232448, "shared memory per CTA (dynamic + the 128 static bytes)");
 };
@@ -302,7 +281,7 @@ __device__ __forceinline__ void add_segment(uint32_t t, int sub, int stride, int
 }
 
 template <bool I8, int TYPE, int CHUNKS>
-__device__ __forceinline__ void store_item(const RaggedParams &p, const Item &it, int sub, int m,
+__device__ __forceinline__ void store_item(const RaggedParams &p, const RaggedItem &it, int sub, int m,
                                            const uint32_t (&acc)[CHUNKS][16]) {
     const float channel = (I8 && m < p.M) ? __ldg(p.channel_scale + static_cast<int64_t>(it.e) * p.M + m) : 1.0f;
 #pragma unroll
@@ -323,7 +302,7 @@ __device__ __forceinline__ void store_item(const RaggedParams &p, const Item &it
 // NA = 2: this thread's 8 chunks of each of the item's two accumulators, packed to 16 bits: columns 2 j and
 // 2 j + 1 of chunk i of accumulator a in pk[a][i][j].
 template <bool I8, int TYPE>
-__device__ __forceinline__ void pack_item(const RaggedParams &p, const Item &it, uint32_t t, int sub, int m,
+__device__ __forceinline__ void pack_item(const RaggedParams &p, const RaggedItem &it, uint32_t t, int sub, int m,
                                           uint32_t (&pk)[2][kRpBN / 32][8]) {
 #pragma unroll
     for (int a = 0; a < 2; ++a) {
@@ -348,8 +327,30 @@ __device__ __forceinline__ void pack_item(const RaggedParams &p, const Item &it,
         }
     }
 }
+// NA = 2, fp32 results: each chunk is stored as it is loaded.
+template <bool I8>
+__device__ __forceinline__ void store_wide_f32(const RaggedParams &p, const RaggedItem &it, uint32_t t, int sub, int m) {
+#pragma unroll
+    for (int a = 0; a < 2; ++a) {
+        const int ma = m + a * kPairRows;
+        const float channel = (I8 && ma < p.M) ? __ldg(p.channel_scale + static_cast<int64_t>(it.e) * p.M + ma) : 1.0f;
+#pragma unroll 2
+        for (int c = 16 * sub; c < it.n_valid; c += 32) {
+            uint32_t r[16];
+            tmem_ld16(t + a * 256 + c, r);
+            tmem_ld_wait();
+            float v[16];
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+                const float row = (I8 && c + j < it.n_valid) ? __ldg(p.row_scale + it.row0 + c + j) : 1.0f;
+                v[j] = ragged_value<I8>(p, r[j], channel, row);
+            }
+            store_cols<BEAM_MOE_F32>(p, it, c, ma, v);
+        }
+    }
+}
 // Neighbouring lanes exchange words so that each stores a pair of features of one row.
-__device__ __forceinline__ void store_packed(const RaggedParams &p, const Item &it, int sub, int m,
+__device__ __forceinline__ void store_packed(const RaggedParams &p, const RaggedItem &it, int sub, int m,
                                              const uint32_t (&pk)[2][kRpBN / 32][8]) {
     const int odd = threadIdx.x & 1;
     const uint32_t sel = odd ? 0x3276u : 0x5410u;  // odd: (neighbour's high half, own), even: (own, neighbour's low half)
@@ -390,7 +391,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kRgThreads, 1)
     uint64_t *drain = acc_empty + C::kSlots;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drain + 1);
     int *tile_start = reinterpret_cast<int *>(smem + C::kTileOff);
-    uint8_t *order = smem + C::kOrderOff;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_ctarank();
@@ -415,7 +415,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kRgThreads, 1)
         tmem_alloc_pair(tmem_slot, 512);
         tmem_relinquish_pair();
     }
-    ragged_items<kRpBN, kRound, false, true>(p, n_mt, false, tile_start, order, reinterpret_cast<int *>(smem));
+    ragged_prefix<kRpBN, false>(p, n_mt, false, tile_start);
     tc_fence_before();
     __syncthreads();
     cluster_sync_all();
@@ -426,15 +426,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kRgThreads, 1)
     if (warp == 0) {
         if (lane == 0) {
             // ---------------- TMA producer: this CTA's features and half of the rows
-            const uint64_t pol_w = p.weights_once ? policy_evict_first() : policy_evict_normal();
-            const uint64_t pol_x = policy_evict_last();
+            const uint64_t pol_once = policy_evict_first(), pol_again = policy_evict_normal();
+            const uint64_t pol_x = policy_evict_last();  // re-read by the other feature tiles
             const uint32_t full_lead = mapa_shared(smem_u32(full), 0);
             constexpr int kElems = I8 ? 128 : 64;  // contraction elements per k-step
             int stage = 0;
             uint32_t phase = 0, issued = 0, issued_phase = 0;
             bool ok = true;
             for (int item = pair; item < total && ok; item += n_pairs) {
-                const Item it = ragged_item<kRpBN, kRound>(item, tile_start, order, p);
+                const RaggedItem it = ragged_item<kRpBN, kRound>(item, tile_start, p);
+                const uint64_t pol_w = it.once ? pol_once : pol_again;
                 const int half = it.n_mma / 2;
                 const int nbox = (half + kRpBox - 1) / kRpBox;
                 const int b_row = static_cast<int>(it.row0) + static_cast<int>(rank) * half;
@@ -481,7 +482,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kRgThreads, 1)
             uint32_t phase = 0, uses = 0;
             bool ok = true;
             for (int item = pair; item < total && ok; item += n_pairs) {
-                const Item it = ragged_item<kRpBN, kRound>(item, tile_start, order, p);
+                const RaggedItem it = ragged_item<kRpBN, kRound>(item, tile_start, p);
                 const uint32_t idesc = idesc_with_n(p.idesc, it.n_mma);
                 for (int kb = 0; kb < p.n_kb && ok;) {
                     const int seg_end = NA == 1 ? min(p.n_kb, kb + p.seg_kb) : p.n_kb;
@@ -533,7 +534,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kRgThreads, 1)
         uint32_t uses = 0;
         bool ok = true;
         for (int item = pair; item < total && ok; item += n_pairs) {
-            const Item it = ragged_item<kRpBN, kRound>(item, tile_start, order, p);
+            const RaggedItem it = ragged_item<kRpBN, kRound>(item, tile_start, p);
             const int m = it.mt * NA * kPairRows + static_cast<int>(rank) * kBM + q * 32 + lane;
             if constexpr (NA == 1) {
                 uint32_t acc[kRpBN / 32][16];
@@ -546,7 +547,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kRgThreads, 1)
                     add_segment<I8, kRpBN / 32>(t0 + (uses & 1) * 256, sub, 32, it.n_valid, kb == 0, acc);
                     tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive_tmem(acc_empty_lead + 8u * (uses & 1));
+                    if (lane == 0) mbar_arrive_async(acc_empty_lead + 8u * (uses & 1));
                 }
                 if (!ok) break;
                 if (p.out_type == BEAM_MOE_BF16) store_item<I8, BEAM_MOE_BF16, kRpBN / 32>(p, it, sub, m, acc);
@@ -557,13 +558,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kRgThreads, 1)
                 ok = mbar_wait(acc_full, uses & 1u, p.timeout);
                 if (!ok) break;
                 tc_fence_after();
-                if (p.out_type == BEAM_MOE_BF16) pack_item<I8, BEAM_MOE_BF16>(p, it, t0, sub, m, pk);
+                if (I8 && p.out_type == BEAM_MOE_F32) store_wide_f32<I8>(p, it, t0, sub, m);
+                else if (p.out_type == BEAM_MOE_BF16) pack_item<I8, BEAM_MOE_BF16>(p, it, t0, sub, m, pk);
                 else pack_item<I8, BEAM_MOE_F16>(p, it, t0, sub, m, pk);
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive_tmem(acc_empty_lead);
+                if (lane == 0) mbar_arrive_async(acc_empty_lead);
                 ++uses;
-                store_packed(p, it, sub, m, pk);
+                if (!I8 || p.out_type != BEAM_MOE_F32) store_packed(p, it, sub, m, pk);
             }
         }
     }
@@ -601,7 +603,7 @@ __device__ __forceinline__ void fence_cluster() { asm volatile("fence.acq_rel.cl
 // This CTA's features of one item: the S partial sums of two neighbouring features per thread, added in
 // rank order, stored as pairs.  buf: [S][BN][F] in this CTA's shared memory, F = 128 / S.
 template <bool I8, int BN, int TYPE>
-__device__ __forceinline__ void reduce_store(const RaggedParams &p, const Item &it, const float *buf, int S, int F,
+__device__ __forceinline__ void reduce_store(const RaggedParams &p, const RaggedItem &it, const float *buf, int S, int F,
                                              int m0, int tid) {
     const int pairs = F / 2;
     for (int idx = tid; idx < it.n_valid * pairs; idx += 32 * kGemmEpiWarps) {
@@ -683,7 +685,7 @@ __global__ void __launch_bounds__(kRgThreads, 1)
         tmem_alloc(tmem_slot, 2 * C::kSlot);
         tmem_relinquish();
     }
-    ragged_items<BN, 16, false, false>(p, n_mt, false, tile_start, nullptr, nullptr);
+    ragged_prefix<BN, false>(p, n_mt, false, tile_start);
     tc_fence_before();
     __syncthreads();
     cluster_sync_all();  // every CTA's barriers are initialised before another one signals them
@@ -693,14 +695,15 @@ __global__ void __launch_bounds__(kRgThreads, 1)
 
     if (warp == 0) {
         if (lane == 0) {
-            const uint64_t pol_w = p.weights_once ? policy_evict_first() : policy_evict_normal();
-            const uint64_t pol_x = policy_evict_last();
+            const uint64_t pol_once = policy_evict_first(), pol_again = policy_evict_normal();
+            const uint64_t pol_x = policy_evict_last();  // re-read by the other feature tiles
             constexpr int kElems = I8 ? 128 : 64;
             int stage = 0;
             uint32_t phase = 0, issued = 0, issued_phase = 0;
             bool ok = true;
             for (int item = cluster; item < total && ok; item += n_clusters) {
-                const Item it = ragged_item<BN, 16>(item, tile_start, nullptr, p);
+                const RaggedItem it = ragged_item<BN, 16>(item, tile_start, p);
+                const uint64_t pol_w = it.once ? pol_once : pol_again;
                 const int nbox = it.n_mma / kRsBox;
                 const int a_row = it.mt * kBM;
                 const uint32_t bytes = static_cast<uint32_t>(kRgOperand + nbox * kRsBox * kRgRowBytes);
@@ -737,7 +740,7 @@ __global__ void __launch_bounds__(kRgThreads, 1)
             uint32_t phase = 0, uses = 0;
             bool ok = true;
             for (int item = cluster; item < total && ok; item += n_clusters) {
-                const Item it = ragged_item<BN, 16>(item, tile_start, nullptr, p);
+                const RaggedItem it = ragged_item<BN, 16>(item, tile_start, p);
                 const uint32_t idesc = idesc_with_n(p.idesc, it.n_mma);
                 for (int kb = kb0; kb < kb1 && ok;) {
                     const int seg_end = min(kb1, kb + p.seg_kb);
@@ -787,7 +790,7 @@ __global__ void __launch_bounds__(kRgThreads, 1)
         uint32_t uses = 0, n_item = 0;
         bool ok = true;
         for (int item = cluster; item < total && ok; item += n_clusters, ++n_item) {
-            const Item it = ragged_item<BN, 16>(item, tile_start, nullptr, p);
+            const RaggedItem it = ragged_item<BN, 16>(item, tile_start, p);
             uint32_t acc[kChunks][16];
             for (int kb = kb0; kb < kb1; kb += p.seg_kb, ++uses) {
                 if (!mbar_wait(&acc_full[uses & 1], (uses >> 1) & 1u, p.timeout)) {
@@ -843,13 +846,11 @@ __global__ void __launch_bounds__(kRgThreads, 1)
 // would: a helper warp clears them in shared memory.  A staged row is one 128-byte line of each box
 // (swizzling permutes within the line), so rows v.. of a box are the contiguous bytes [128 v, ...), and
 // only the rows up to the next multiple of 16 (one instruction's contraction) are cleared and multiplied.
-//   full[s] (leader)  a whole k-step's loads of both CTAs complete on it directly; for a k-step to clear the
-//                     leader's helper arrives on it once both CTAs have cleared theirs
-//   tail[s]           this CTA's loads of a k-step to clear have landed
-//   cleared[s] (leader)  the peer's helper has cleared its part
-// No thread arrives on the other CTA's barriers for a whole k-step: a remote arrival releases at cluster
-// scope, which waits for the thread's earlier memory operations, and one per k-step held the ring at 700
-// TFLOP/s (with or without the products themselves).
+//   full[s] (leader, two arrivals)  a whole k-step's loads of both CTAs complete on it directly, both
+//            arrivals being the leader's producer's; for a k-step to clear the two helpers arrive on it
+//   tail[s]  this CTA's loads of a k-step to clear have landed
+// No producer arrives on the other CTA's barrier: one such release at cluster scope per k-step, which waits
+// for the thread's earlier memory operations, held the ring at 700 TFLOP/s (with or without the products).
 // The epilogue converts 32 rows x 128 bytes per warp into a swizzled staging buffer and stores it with
 // TMA, which clips at N and K; `accumulate` stores with TMA's FP32 add.  Groups without rows store zeros.
 // With `splits` > 1 split s takes its share of each group's k-steps and stores FP32 partial sums at group
@@ -860,9 +861,8 @@ constexpr int kRwStageOut = 4096;  // one staged output chunk: 32 rows of 128 by
 constexpr int kRwOutOff = kRwStages * 2 * kRgOperand;
 constexpr int kRwBarOff = kRwOutOff + kGemmEpiWarps * 2 * kRwStageOut;
 constexpr int kRwTileOff = kRwBarOff + 256;
-constexpr int kRwOrderOff = kRwTileOff + 4 * (kPmMaxE + 1);
-constexpr int kRwSmem = 1024 + kRwOrderOff + kPmMaxE + 60;
-static_assert(8 * (4 * kRwStages + 2 * 2 + 1) + 4 <= 256, "barrier area");
+constexpr int kRwSmem = 1024 + kRwTileOff + 4 * (kPmMaxE + 1) + 64;
+static_assert(8 * (3 * kRwStages + 2 * 2 + 1) + 4 <= 256, "barrier area");
 static_assert(kRwSmem + 128 <= 232448, "shared memory per CTA (dynamic + the 128 static bytes)");
 
 struct WgradItem {
@@ -877,12 +877,10 @@ struct WgradParams {
     int accumulate;  // FP32 output: add to it, groups without rows are left alone
 };
 
-__device__ __forceinline__ WgradItem wgrad_item(int item, const int *tile_start, const uint8_t *order,
-                                                const WgradParams &p) {
+__device__ __forceinline__ WgradItem wgrad_item(int item, const int *tile_start, const WgradParams &p) {
     WgradItem it;
-    const int place = find_place(item, tile_start, p.g.E);
-    it.e = order[place];
-    int local = item - tile_start[place];
+    it.e = find_group(item, tile_start, p.g.E);
+    int local = item - tile_start[it.e];
     const int n_mt = (p.g.M + kPairRows - 1) / kPairRows;
     const int split = local / (n_mt * p.n_nt);
     local -= split * n_mt * p.n_nt;
@@ -980,11 +978,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kRwThreads, 1)
     uint64_t *acc_full = empty + kRwStages;
     uint64_t *acc_empty = acc_full + 2;
     uint64_t *tail = acc_empty + 2;
-    uint64_t *cleared = tail + kRwStages;
-    uint64_t *drain = cleared + kRwStages;
+    uint64_t *drain = tail + kRwStages;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drain + 1);
     int *tile_start = reinterpret_cast<int *>(smem + kRwTileOff);
-    uint8_t *order = smem + kRwOrderOff;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_ctarank();
@@ -994,10 +990,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kRwThreads, 1)
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < kRwStages; ++s) {
-            mbar_init(&full[s], 1);
+            mbar_init(&full[s], 2);
             mbar_init(&empty[s], 1);
             mbar_init(&tail[s], 1);
-            mbar_init(&cleared[s], 1);
         }
         for (int a = 0; a < 2; ++a) {
             mbar_init(&acc_full[a], 1);
@@ -1013,8 +1008,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kRwThreads, 1)
         tmem_alloc_pair(tmem_slot, 512);
         tmem_relinquish_pair();
     }
-    ragged_items<256, 16, true, true>(p.g, n_mt * p.n_nt * p.splits, p.accumulate != 0, tile_start, order,
-                                      reinterpret_cast<int *>(smem));
+    ragged_prefix<256, true>(p.g, n_mt * p.n_nt * p.splits, p.accumulate != 0, tile_start);
     tc_fence_before();
     __syncthreads();
     cluster_sync_all();
@@ -1032,7 +1026,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kRwThreads, 1)
             uint32_t phase = 0, issued = 0, issued_phase = 0;
             bool ok = true;
             for (int item = pair; item < total && ok; item += n_pairs) {
-                const WgradItem it = wgrad_item(item, tile_start, order, p);
+                const WgradItem it = wgrad_item(item, tile_start, p);
                 const int a_col = it.n0 + static_cast<int>(rank) * kBM;
                 const int b_col = it.k0 + static_cast<int>(rank) * (it.n_mma / 2);
                 const int nbox = it.n_mma / 128;  // 64-column boxes of x per CTA
@@ -1050,6 +1044,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kRwThreads, 1)
                         mbar_arrive_expect_tx(&tail[stage], bytes);
                     } else if (rank == 0) {
                         mbar_arrive_expect_tx(&full[stage], 2u * bytes);
+                        mbar_arrive(&full[stage]);
                     }
                     tma_load_2d_pair(sa, &tm_dy, bar, a_col, row, pol);
                     tma_load_2d_pair(sa + kRgOperand / 2, &tm_dy, bar, a_col + 64, row, pol);
@@ -1073,7 +1068,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kRwThreads, 1)
             uint32_t phase = 0, uses = 0;
             bool ok = true;
             for (int item = pair; item < total && ok; item += n_pairs) {
-                const WgradItem it = wgrad_item(item, tile_start, order, p);
+                const WgradItem it = wgrad_item(item, tile_start, p);
                 const uint32_t idesc = idesc_with_n(p.g.idesc, it.n_mma);
                 const int n_kb = (it.rows + 63) / 64;
                 for (int kb = 0; kb < n_kb && ok;) {
@@ -1111,10 +1106,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kRwThreads, 1)
         }
     } else if (warp == 2) {
         // ---------------- helper: clears the rows behind the group in its last k-step
-        const uint32_t cleared_lead = mapa_shared(smem_u32(cleared), 0);
-        uint32_t steps = 0, phases = 0;  // k-steps up to this item's end; per stage, the phase of tail and cleared
+        const uint32_t full_lead = mapa_shared(smem_u32(full), 0);
+        uint32_t steps = 0, phases = 0;  // k-steps up to this item's end; per stage, the phase of `tail`
         for (int item = pair; item < total; item += n_pairs) {
-            const WgradItem it = wgrad_item(item, tile_start, order, p);
+            const WgradItem it = wgrad_item(item, tile_start, p);
             if (it.rows == 0) continue;
             const uint32_t n_kb = static_cast<uint32_t>((it.rows + 63) / 64);
             steps += n_kb;
@@ -1133,12 +1128,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kRwThreads, 1)
             }
             fence_proxy_async_smem();
             __syncwarp();
-            if (rank != 0) {
-                if (lane == 0) mbar_arrive_cluster(cleared_lead + 8u * stage);
-            } else {
-                if (!mbar_wait_cluster(&cleared[stage], phase, timeout)) break;
-                if (lane == 0) mbar_arrive(&full[stage]);
-            }
+            if (lane == 0) mbar_arrive_async(full_lead + 8u * stage);
         }
     } else if (warp >= 4) {
         // ---------------- epilogue: lanes = rows n, two warps per quadrant share the product's columns
@@ -1148,7 +1138,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kRwThreads, 1)
         uint32_t uses = 0, n_out = 0;
         bool ok = true;
         for (int item = pair; item < total && ok; item += n_pairs) {
-            const WgradItem it = wgrad_item(item, tile_start, order, p);
+            const WgradItem it = wgrad_item(item, tile_start, p);
             const int n_kb = (it.rows + 63) / 64;
             const int cols = it.n_mma / 2;  // this warp's columns: [cols sub, cols (sub + 1))
             uint32_t acc[8][16];
@@ -1168,7 +1158,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kRwThreads, 1)
                 add_segment<false, 8>(t, 0, 16, cols, kb == 0, acc);
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive_tmem(acc_empty_lead + 8u * (uses & 1));
+                if (lane == 0) mbar_arrive_async(acc_empty_lead + 8u * (uses & 1));
             }
             if (!ok) break;
             const int n = it.n0 + static_cast<int>(rank) * kBM + q * 32;

@@ -176,7 +176,7 @@ struct RaggedPlan {
     int S, log_s;  // split kernels: CTAs per cluster
     int items;
 };
-RaggedPlan ragged_plan(const RaggedDevice &d, int E, int64_t R, int M, int n_kb, bool out16) {
+RaggedPlan ragged_plan(const RaggedDevice &d, int E, int64_t R, int M, int n_kb, bool wide_ok) {
     RaggedPlan P{};
     const int64_t groups = std::min<int64_t>(E, R);
     const int64_t mean = (R + groups - 1) / groups;
@@ -185,9 +185,10 @@ RaggedPlan ragged_plan(const RaggedDevice &d, int E, int64_t R, int M, int n_kb,
     P.few = mean <= 32;
     if (!P.few && pair_items >= d.pairs) {
         P.pair = 1;
-        // two feature tiles per pair where groups span several row tiles and the rounds come out shorter: a
-        // k-step costs ~690 cycles with one, ~1060 with two, whose epilogue adds ~2000 per item
-        if (out16 && mean > kRpBN) {
+        // two feature tiles per pair where the rounds come out shorter: a k-step costs ~690 cycles with one,
+        // ~1060 with two, whose epilogue adds ~2000 per item (256 groups of 30 to 500 rows, 5120 x 2560:
+        // 1.25 against 1.36 ms; 64 groups of 80 to 900: 0.47 against 0.56)
+        if (wide_ok) {
             const int64_t wide_items = row_tiles * ((M + 2 * kPairRows - 1) / (2 * kPairRows));
             const int64_t t1 = (pair_items + d.pairs - 1) / d.pairs * n_kb * 690;
             const int64_t t2 = (wide_items + d.pairs - 1) / d.pairs * (n_kb * int64_t(1060) + 2000);
@@ -247,9 +248,7 @@ int ragged_product(const RaggedCall &c, cudaStream_t s) {
     if (!encode_fn()) return BEAM_MOE_ERR_CUDA;
     const int kelems = kRgRowBytes / esize;
     const int n_kb = (width + kelems - 1) / kelems;
-    const RaggedPlan P = ragged_plan(d, c.E, c.R, M, n_kb, c.out_type != BEAM_MOE_F32);
-    const int bn = P.pair ? kRpBN : (P.few ? 32 : 128);
-    const double mean = static_cast<double>(c.R) / static_cast<double>(std::min<int64_t>(c.E, c.R));
+    const RaggedPlan P = ragged_plan(d, c.E, c.R, M, n_kb, c.i8 || c.out_type != BEAM_MOE_F32);
     RaggedParams p{};
     p.offsets = c.offsets;
     p.out = c.out;
@@ -261,7 +260,6 @@ int ragged_product(const RaggedCall &c, cudaStream_t s) {
     p.seg_kb = segment_steps(c.i8, c.out_type, n_kb);
     p.out_type = c.out_type;
     p.idesc = ragged_idesc(c.i8, c.dtype, P.pair ? kPairRows : kBM, c.dgrad, false);
-    p.weights_once = mean + 4.0 * std::sqrt(mean) <= bn ? 1 : 0;
     p.row_scale = c.row_scale;
     p.channel_scale = c.channel_scale;
     p.timeout = kDefaultTimeoutCycles;
