@@ -14,10 +14,10 @@
 // dgrad reads the same [E, N, K] weights: their tile is the MMA's MN-major A operand, so no
 // transposed copy of the weights exists.  wgrad contracts over the rows: both operands are MN-major.
 //
-// Accumulation.  The tensor core's FP32 accumulator rounds toward zero at each instruction (measured
-// on 5120-long sums: 1e-5 relative, all toward zero), so long sums are cut into segments of `seg_kb`
-// k-steps: each segment accumulates in its own TMEM slot and the epilogue adds the segments in FP32
-// registers with round-to-nearest, while the next segment's products run in the other slot.
+// Accumulation.  The tensor core truncates its FP32 running sum at each instruction, so long sums are cut into
+// segments of `seg_kb` k-steps: each accumulates in its own TMEM slot, and the epilogue adds the segments in
+// FP32 registers, to nearest, while the next one's products run in the other slot (segment_steps and
+// one_segment_ok in ragged_api.cuh say how long they are and why).
 //
 // Every mbarrier wait is bounded (status word BEAM_MOE_ERR_DEVICE_TIMEOUT on expiry); offsets that do
 // not ascend within [0, R] set BEAM_MOE_ERR_BAD_INDEX and nothing is written; no load uses multicast.
@@ -840,9 +840,9 @@ __global__ void __launch_bounds__(kRgThreads, 1)
 }
 
 // ---- wgrad on CTA pairs ----------------------------------------------------------------------------
-// dw[e][n][k] tiles of 256 x 256: the contraction runs over the group's rows in k-steps of 64, dy^T is the
-// MMA's A (CTA r: columns n 128 r..), x^T its B (CTA r: half of the columns k), both MN-major.  The rows of
-// a group's last k-step that belong to the next group must not enter the sums, and zero times a NaN there
+// dw[e][n][k] tiles of 256 x 256 NB: the contraction runs over the group's rows in k-steps of 64, dy^T is the
+// MMA's A (CTA r: columns n 128 r..), x^T its B (CTA r: half of each 256 columns k), both MN-major.  The rows
+// of a group's last k-step that belong to the next group must not enter the sums, and zero times a NaN there
 // would: a helper warp clears them in shared memory.  A staged row is one 128-byte line of each box
 // (swizzling permutes within the line), so rows v.. of a box are the contiguous bytes [128 v, ...), and
 // only the rows up to the next multiple of 16 (one instruction's contraction) are cleared and multiplied.
@@ -851,60 +851,86 @@ __global__ void __launch_bounds__(kRgThreads, 1)
 //   tail[s]  this CTA's loads of a k-step to clear have landed
 // No producer arrives on the other CTA's barrier: one such release at cluster scope per k-step, which waits
 // for the thread's earlier memory operations, held the ring at 700 TFLOP/s (with or without the products).
-// The epilogue converts 32 rows x 128 bytes per warp into a swizzled staging buffer and stores it with
-// TMA, which clips at N and K; `accumulate` stores with TMA's FP32 add.  Groups without rows store zeros.
+//
+// The epilogue stages 32 rows x 128 bytes per warp at a time, swizzled, and stores them with TMA, which clips
+// at N and K and, for `accumulate`, adds (FP32).  Groups without rows store zeros.
+//   NB = 1: 5 stages of 16 KB + 16 KB, two TMEM slots, two staging buffers per warp; sums longer than
+//     seg_kb k-steps are cut into segments, added in registers.
+//   NB = 2: 4 stages of 16 KB + 2 x 16 KB, so a quarter fewer bytes from L2, which bounds both long groups
+//     (L2 to the SMs) and short ones (loads and stores together); one item fills TMEM and each warp has one
+//     staging buffer.  fp32 results of more than seg_kb k-steps are flushed by TMA adds.
 // With `splits` > 1 split s takes its share of each group's k-steps and stores FP32 partial sums at group
 // index s E + e of a [splits E][N][K] workspace, which ragged_join_kernel adds in order.
-constexpr int kRwThreads = 384;  // warp 0 TMA, warp 1 MMA, warp 2 helper, warp 3 idle, warps 4..11 epilogue
-constexpr int kRwStages = 5;
+constexpr int kRwThreads = 384;    // warp 0 TMA, warp 1 MMA, warp 2 helper, warp 3 idle, warps 4..11 epilogue
 constexpr int kRwStageOut = 4096;  // one staged output chunk: 32 rows of 128 bytes
-constexpr int kRwOutOff = kRwStages * 2 * kRgOperand;
-constexpr int kRwBarOff = kRwOutOff + kGemmEpiWarps * 2 * kRwStageOut;
-constexpr int kRwTileOff = kRwBarOff + 256;
-constexpr int kRwSmem = 1024 + kRwTileOff + 4 * (kPmMaxE + 1) + 64;
-static_assert(8 * (3 * kRwStages + 2 * 2 + 1) + 4 <= 256, "barrier area");
-static_assert(kRwSmem + 128 <= 232448, "shared memory per CTA (dynamic + the 128 static bytes)");
+template <int NB>
+struct RwgradCfg {
+    static constexpr int kStages = NB == 1 ? 5 : 4;
+    static constexpr int kStage = (1 + NB) * kRgOperand;
+    static constexpr int kSlots = NB == 1 ? 2 : 1;
+    static constexpr int kOutBufs = NB == 1 ? 2 : 1;  // per warp
+    static constexpr int kOutOff = kStages * kStage;
+    static constexpr int kBarOff = kOutOff + kGemmEpiWarps * kOutBufs * kRwStageOut;
+    static constexpr int kTileOff = kBarOff + 256;
+    static constexpr int kSmem = 1024 + kTileOff + 4 * (kPmMaxE + 1) + 64;
+    static_assert(8 * (3 * kStages + 2 * kSlots + 1) + 4 <= 256, "barrier area");
+    static_assert(kSmem + 128 <= 232448, "shared memory per CTA (dynamic + the 128 static bytes)");
+};
 
 struct WgradItem {
-    int e, n0, k0, n_mma;  // n_mma: columns of the pair's product (128 or 256)
+    int e, n0, k0;
     int group;             // group index of the stored tile: split * E + e
     int64_t row0;
     int rows;              // rows of this item's share of the group (its first row is row0)
 };
 struct WgradParams {
     RaggedParams g;  // M = N of the product; n_kb unused
-    int K, n_nt, splits;
+    int K, n_mt, n_nt, splits;
+    uint32_t nt_inv;  // ceil(2^32 / n_nt): local / n_nt = local * nt_inv >> 32, exact for local * n_nt < 2^32
     int accumulate;  // FP32 output: add to it, groups without rows are left alone
 };
 
-__device__ __forceinline__ WgradItem wgrad_item(int item, const int *tile_start, const WgradParams &p) {
+// Item `item` (of ascending ones; `e` walks along).  Every role decodes every item, and a short group's item
+// is over in ~2000 cycles: no search from the start and no slow division here (with both, 64 groups of 32
+// rows took 320 us instead of 250).
+template <int NB>
+__device__ __forceinline__ WgradItem wgrad_item(int item, int &e, const int *tile_start, const WgradParams &p) {
     WgradItem it;
-    it.e = find_group(item, tile_start, p.g.E);
-    int local = item - tile_start[it.e];
-    const int n_mt = (p.g.M + kPairRows - 1) / kPairRows;
-    const int split = local / (n_mt * p.n_nt);
-    local -= split * n_mt * p.n_nt;
-    const int mt = local / p.n_nt;
-    it.n0 = mt * kPairRows;
-    it.k0 = (local - mt * p.n_nt) * 256;
-    it.n_mma = p.K - it.k0 > 128 ? 256 : 128;
-    it.group = split * p.g.E + it.e;
-    const int rows = group_rows(p.g, it.e);
-    const int64_t steps = (rows + 63) / 64;
-    const int r0 = static_cast<int>(steps * split / p.splits) * 64;
-    const int r1 = min(rows, static_cast<int>(steps * (split + 1) / p.splits) * 64);
-    it.row0 = group_begin(p.g, it.e) + r0;
-    it.rows = max(0, r1 - r0);
+    while (tile_start[e + 1] <= item) ++e;
+    it.e = e;
+    uint32_t local = static_cast<uint32_t>(item - tile_start[e]);
+    const int rows = group_rows(p.g, e);
+    it.row0 = group_begin(p.g, e);
+    it.rows = rows;
+    it.group = e;
+    if (p.splits > 1) {
+        const uint32_t tiles = static_cast<uint32_t>(p.n_mt * p.n_nt), split = local / tiles;
+        const uint32_t steps = static_cast<uint32_t>((rows + 63) / 64), n = static_cast<uint32_t>(p.splits);
+        local -= split * tiles;
+        const int r0 = static_cast<int>(steps * split / n) * 64;  // steps <= 2^18, splits <= 64
+        const int r1 = min(rows, static_cast<int>(steps * (split + 1) / n) * 64);
+        it.row0 += r0;
+        it.rows = max(0, r1 - r0);
+        it.group = static_cast<int>(split) * p.g.E + e;
+    }
+    const uint32_t mt = p.n_nt == 1 ? local : __umulhi(local, p.nt_inv);
+    it.n0 = static_cast<int>(mt) * kPairRows;
+    it.k0 = static_cast<int>(local - mt * static_cast<uint32_t>(p.n_nt)) * (256 * NB);
     return it;
 }
+// Columns of the product at column k0 of K (256, or 128 where no more are left; 0: none).
+__device__ __forceinline__ int wgrad_cols(int k0, int K) { return K - k0 > 128 ? 256 : (K > k0 ? 128 : 0); }
 
 // A k-step of v rows of the group (64 or more: whole): whether its last instruction meets rows behind it.
 __device__ __forceinline__ bool needs_clearing(int v) { return v < 64 && (v & 15); }
 
-__device__ __forceinline__ void tma_store_3d(const CUtensorMap *map, const void *src, int c0, int c1, int c2) {
-    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(map), "r"(c0),
-                 "r"(c1), "r"(c2), "r"(smem_u32(src))
-                 : "memory");
+// (evict-first: results of a size that does not stay in L2 anyway, 6% off the fp32 case)
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap *map, const void *src, int c0, int c1, int c2,
+                                             uint64_t policy) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.global.shared::cta.bulk_group.L2::cache_hint [%0, {%1, %2, %3}], [%4], %5;" ::"l"(map),
+        "r"(c0), "r"(c1), "r"(c2), "r"(smem_u32(src)), "l"(policy)
+        : "memory");
 }
 __device__ __forceinline__ void tma_add_3d(const CUtensorMap *map, const void *src, int c0, int c1, int c2) {
     asm volatile("cp.reduce.async.bulk.tensor.3d.global.shared::cta.add.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(map),
@@ -922,79 +948,130 @@ __device__ __forceinline__ void sts128(uint32_t addr, uint4 v) {
                  : "memory");
 }
 
-// The warp's 32 rows (one per lane) x 128 columns of accumulators: staged 128 bytes per row at a time,
-// swizzled as the tensor map expects, and stored by TMA.  Two staging buffers per warp.
-template <int TYPE>
-__device__ __forceinline__ void wgrad_store(const CUtensorMap *map, const WgradItem &it, int n, int k, int k_end,
-                                            int accumulate, uint32_t stage, const uint8_t *stage_ptr,
-                                            uint32_t &n_out, const uint32_t (&acc)[8][16]) {
+// A warp's output: 128 bytes of each of its 32 rows (one per lane) at a time go through a staging buffer.
+template <int BUFS>
+struct WgradOut {
+    const CUtensorMap *map;
+    uint8_t *stage;
+    uint64_t policy;
+    uint32_t n_out;  // chunks so far
+
+    // Columns k.. of rows n.. of group `group`; word(i): the i-th of this lane's 32 words.
+    template <typename F>
+    __device__ __forceinline__ void chunk(int k, int n, int group, bool add, F word) {
+        const int lane = threadIdx.x & 31;
+        uint8_t *src = stage + (BUFS == 1 ? 0 : (n_out & 1) * kRwStageOut);
+        ++n_out;
+        if (lane == 0) bulk_wait_read<BUFS - 1>();  // the store that last used this buffer has read it
+        __syncwarp();
+        const uint32_t buf = smem_u32(src) + lane * 128;
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            sts128(buf + ((j ^ (lane & 7)) << 4),
+                   make_uint4(word(4 * j), word(4 * j + 1), word(4 * j + 2), word(4 * j + 3)));
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+            if (add) tma_add_3d(map, src, k, n, group);
+            else tma_store_3d(map, src, k, n, group, policy);
+            bulk_commit();
+        }
+    }
+};
+
+// 128 columns (those below k_end) of fp32 accumulators, in `TYPE`.
+template <int TYPE, int BUFS>
+__device__ __forceinline__ void wgrad_store(WgradOut<BUFS> &out, int group, int n, int k, int k_end, bool add,
+                                            const uint32_t (&acc)[8][16]) {
     constexpr int kCols = TYPE == BEAM_MOE_F32 ? 32 : 64;  // columns per 128 bytes
-    const int lane = threadIdx.x & 31;
 #pragma unroll
     for (int b = 0; b < 128 / kCols; ++b) {
         if (k + b * kCols < k_end) {  // warp-uniform
-            const uint32_t at = (n_out++ & 1) * kRwStageOut;
-            const uint32_t buf = stage + at + lane * 128;
-            if (lane == 0) bulk_wait_read<1>();  // the store before the last one has left this buffer
-            __syncwarp();
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {  // 16 bytes each
-                uint4 v;
-                uint32_t *w = reinterpret_cast<uint32_t *>(&v);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    if constexpr (TYPE == BEAM_MOE_F32) {
-                        const int c = b * 32 + j * 4 + i;
-                        w[i] = acc[c / 16][c % 16];
-                    } else {
-                        const int c = b * 64 + j * 8 + 2 * i;
-                        w[i] = pack2<TYPE>(__uint_as_float(acc[c / 16][c % 16]),
-                                           __uint_as_float(acc[c / 16][c % 16 + 1]));
-                    }
+            out.chunk(k + b * kCols, n, group, add, [&](int i) {
+                if constexpr (TYPE == BEAM_MOE_F32) {
+                    const int c = b * 32 + i;
+                    return acc[c / 16][c % 16];
+                } else {
+                    const int c = b * 64 + 2 * i;
+                    return pack2<TYPE>(__uint_as_float(acc[c / 16][c % 16]), __uint_as_float(acc[c / 16][c % 16 + 1]));
                 }
-                sts128(buf + ((j ^ (lane & 7)) << 4), v);
-            }
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) {
-                const uint8_t *src = stage_ptr + at;
-                if (accumulate) tma_add_3d(map, src, k + b * kCols, n, it.group);
-                else tma_store_3d(map, src, k + b * kCols, n, it.group);
-                bulk_commit();
-            }
+            });
         }
     }
 }
 
+// NB = 2, 16-bit results: the two products' accumulators packed to 16 bits, TMEM handed back, then stored.
+template <int TYPE>
+__device__ __forceinline__ void wgrad_pack_store(WgradOut<1> &out, const WgradItem &it, int K, int sub, int n, bool live,
+                                                 bool rows, uint32_t t0, uint32_t acc_empty_lead) {
+    uint32_t pk[2][8][8];
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+        const int cols = wgrad_cols(it.k0 + 256 * b, K) / 2;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            if (rows && 16 * i < cols) {  // warp-uniform
+                uint32_t r[16];
+                tmem_ld16(t0 + 256 * b + cols * sub + 16 * i, r);
+                tmem_ld_wait();
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    pk[b][i][j] = pack2<TYPE>(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1]));
+            } else {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) pk[b][i][j] = 0u;
+            }
+        }
+    }
+    if (rows) {
+        tc_fence_before();
+        __syncwarp();
+        if ((threadIdx.x & 31) == 0) mbar_arrive_async(acc_empty_lead);
+    }
+    if (!live) return;
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+        const int cols = wgrad_cols(it.k0 + 256 * b, K) / 2;
+        const int k = it.k0 + 256 * b + cols * sub, k_end = min(K, k + cols);
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+            if (k + 64 * c < k_end)
+                out.chunk(k + 64 * c, n, it.group, false, [&](int i) { return pk[b][c * 4 + i / 8][i % 8]; });
+        }
+    }
+}
+
+template <int NB>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kRwThreads, 1)
     ragged_wgrad_kernel(const __grid_constant__ CUtensorMap tm_dy,  // [R][N], box 64 x 64
                         const __grid_constant__ CUtensorMap tm_x,   // [R][K], box 64 x 64
                         const __grid_constant__ CUtensorMap tm_dw,  // [groups][N][K], box 32 rows x 128 bytes
                         const WgradParams p) {
+    using C = RwgradCfg<NB>;
+    constexpr int kStages = C::kStages;
     extern __shared__ uint8_t gemm_smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(gemm_smem_raw) + 1023) & ~uintptr_t(1023));
-    uint64_t *full = reinterpret_cast<uint64_t *>(smem + kRwBarOff);
-    uint64_t *empty = full + kRwStages;
-    uint64_t *acc_full = empty + kRwStages;
-    uint64_t *acc_empty = acc_full + 2;
-    uint64_t *tail = acc_empty + 2;
-    uint64_t *drain = tail + kRwStages;
+    uint64_t *full = reinterpret_cast<uint64_t *>(smem + C::kBarOff);
+    uint64_t *empty = full + kStages;
+    uint64_t *acc_full = empty + kStages;
+    uint64_t *acc_empty = acc_full + C::kSlots;
+    uint64_t *tail = acc_empty + C::kSlots;
+    uint64_t *drain = tail + kStages;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drain + 1);
-    int *tile_start = reinterpret_cast<int *>(smem + kRwTileOff);
+    int *tile_start = reinterpret_cast<int *>(smem + C::kTileOff);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_ctarank();
     const int pair = static_cast<int>(cluster_id_x()), n_pairs = static_cast<int>(cluster_count_x());
-    const int n_mt = (p.g.M + kPairRows - 1) / kPairRows;
     const long long timeout = p.g.timeout;
 
     if (threadIdx.x == 0) {
-        for (int s = 0; s < kRwStages; ++s) {
+        for (int s = 0; s < kStages; ++s) {
             mbar_init(&full[s], 2);
             mbar_init(&empty[s], 1);
             mbar_init(&tail[s], 1);
         }
-        for (int a = 0; a < 2; ++a) {
+        for (int a = 0; a < C::kSlots; ++a) {
             mbar_init(&acc_full[a], 1);
             mbar_init(&acc_empty[a], 2 * kGemmEpiWarps);
         }
@@ -1008,7 +1085,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kRwThreads, 1)
         tmem_alloc_pair(tmem_slot, 512);
         tmem_relinquish_pair();
     }
-    ragged_prefix<256, true>(p.g, n_mt * p.n_nt * p.splits, p.accumulate != 0, tile_start);
+    ragged_prefix<256, true>(p.g, p.n_mt * p.n_nt * p.splits, p.accumulate != 0, tile_start);
     tc_fence_before();
     __syncthreads();
     cluster_sync_all();
@@ -1025,18 +1102,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kRwThreads, 1)
             int stage = 0;
             uint32_t phase = 0, issued = 0, issued_phase = 0;
             bool ok = true;
-            for (int item = pair; item < total && ok; item += n_pairs) {
-                const WgradItem it = wgrad_item(item, tile_start, p);
+            for (int item = pair, e = 0; item < total && ok; item += n_pairs) {
+                const WgradItem it = wgrad_item<NB>(item, e, tile_start, p);
                 const int a_col = it.n0 + static_cast<int>(rank) * kBM;
-                const int b_col = it.k0 + static_cast<int>(rank) * (it.n_mma / 2);
-                const int nbox = it.n_mma / 128;  // 64-column boxes of x per CTA
-                const uint32_t bytes = static_cast<uint32_t>(kRgOperand + nbox * (kRgOperand / 2));
+                int nbox[NB], b_col[NB];  // 64-column boxes of x per CTA
+                int boxes = 2;
+#pragma unroll
+                for (int j = 0; j < NB; ++j) {
+                    const int cols = wgrad_cols(it.k0 + 256 * j, p.K);
+                    nbox[j] = cols / 128;
+                    b_col[j] = it.k0 + 256 * j + static_cast<int>(rank) * (cols / 2);
+                    boxes += nbox[j];
+                }
+                const uint32_t bytes = static_cast<uint32_t>(boxes * (kRgOperand / 2));
                 for (int r = 0; r < it.rows; r += 64) {
                     if (!mbar_wait(&empty[stage], phase ^ 1u, timeout)) {
                         ok = false;
                         break;
                     }
-                    uint8_t *sa = smem + stage * 2 * kRgOperand;
+                    uint8_t *sa = smem + stage * C::kStage;
                     const int row = static_cast<int>(it.row0) + r;
                     uint32_t bar = full_lead + 8u * static_cast<uint32_t>(stage);
                     if (needs_clearing(it.rows - r)) {
@@ -1048,17 +1132,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kRwThreads, 1)
                     }
                     tma_load_2d_pair(sa, &tm_dy, bar, a_col, row, pol);
                     tma_load_2d_pair(sa + kRgOperand / 2, &tm_dy, bar, a_col + 64, row, pol);
-                    for (int b = 0; b < nbox; ++b)
-                        tma_load_2d_pair(sa + kRgOperand + b * (kRgOperand / 2), &tm_x, bar, b_col + 64 * b, row, pol);
+#pragma unroll
+                    for (int j = 0; j < NB; ++j)
+                        for (int b = 0; b < nbox[j]; ++b)
+                            tma_load_2d_pair(sa + (1 + j) * kRgOperand + b * (kRgOperand / 2), &tm_x, bar,
+                                             b_col[j] + 64 * b, row, pol);
                     issued |= 1u << stage;
                     issued_phase = (issued_phase & ~(1u << stage)) | (phase << stage);
-                    if (++stage == kRwStages) {
+                    if (++stage == kStages) {
                         stage = 0;
                         phase ^= 1u;
                     }
                 }
             }
-            for (int s = 0; s < kRwStages; ++s)
+            for (int s = 0; s < kStages; ++s)
                 if ((issued >> s) & 1u) mbar_wait(&empty[s], (issued_phase >> s) & 1u, timeout);
         }
     } else if (warp == 1) {
@@ -1067,37 +1154,50 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kRwThreads, 1)
             int stage = 0;
             uint32_t phase = 0, uses = 0;
             bool ok = true;
-            for (int item = pair; item < total && ok; item += n_pairs) {
-                const WgradItem it = wgrad_item(item, tile_start, p);
-                const uint32_t idesc = idesc_with_n(p.g.idesc, it.n_mma);
+            for (int item = pair, e = 0; item < total && ok; item += n_pairs) {
+                const WgradItem it = wgrad_item<NB>(item, e, tile_start, p);
+                uint32_t idesc[NB];
+                int n_b = 0;  // products of the item
+#pragma unroll
+                for (int j = 0; j < NB; ++j) {
+                    const int cols = wgrad_cols(it.k0 + 256 * j, p.K);
+                    idesc[j] = idesc_with_n(p.g.idesc, cols);
+                    n_b += cols > 0;
+                }
                 const int n_kb = (it.rows + 63) / 64;
                 for (int kb = 0; kb < n_kb && ok;) {
                     const int seg_end = min(n_kb, kb + p.g.seg_kb);
-                    if (!mbar_wait(&acc_empty[uses & 1], ((uses >> 1) & 1u) ^ 1u, timeout)) {
+                    const uint32_t slot = uses % C::kSlots;
+                    if (!mbar_wait(&acc_empty[slot], ((uses / C::kSlots) & 1u) ^ 1u, timeout)) {
                         ok = false;
                         break;
                     }
                     tc_fence_after();
-                    const uint32_t d = tmem_base + (uses & 1) * 256;
+                    const uint32_t d = tmem_base + slot * 256;
                     for (bool first = true; kb < seg_end; ++kb, first = false) {
                         if (!mbar_wait(&full[stage], phase, timeout)) {
                             ok = false;
                             break;
                         }
                         tc_fence_after();
-                        const uint32_t sa = smem_u32(smem + stage * 2 * kRgOperand);
-                        const uint64_t da = umma_desc_mn_sw128(sa), db = umma_desc_mn_sw128(sa + kRgOperand);
+                        const uint32_t sa = smem_u32(smem + stage * C::kStage);
+                        const uint64_t da = umma_desc_mn_sw128(sa);
                         const int n_mma16 = min(4, (it.rows - kb * 64 + 15) / 16);
                         for (int kk = 0; kk < n_mma16; ++kk)
-                            umma_bf16_pair(d, da + 128 * kk, db + 128 * kk, idesc, (!first || kk > 0) ? 1u : 0u);
+#pragma unroll
+                            for (int j = 0; j < NB; ++j)
+                                if (j < n_b)
+                                    umma_bf16_pair(d + 256 * j, da + 128 * kk,
+                                                   umma_desc_mn_sw128(sa + (1 + j) * kRgOperand) + 128 * kk, idesc[j],
+                                                   (!first || kk > 0) ? 1u : 0u);
                         umma_commit_pair_both(&empty[stage]);
-                        if (++stage == kRwStages) {
+                        if (++stage == kStages) {
                             stage = 0;
                             phase ^= 1u;
                         }
                     }
                     if (!ok) break;
-                    umma_commit_pair_both(&acc_full[uses & 1]);
+                    umma_commit_pair_both(&acc_full[slot]);
                     ++uses;
                 }
             }
@@ -1108,21 +1208,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kRwThreads, 1)
         // ---------------- helper: clears the rows behind the group in its last k-step
         const uint32_t full_lead = mapa_shared(smem_u32(full), 0);
         uint32_t steps = 0, phases = 0;  // k-steps up to this item's end; per stage, the phase of `tail`
-        for (int item = pair; item < total; item += n_pairs) {
-            const WgradItem it = wgrad_item(item, tile_start, p);
+        for (int item = pair, e = 0; item < total; item += n_pairs) {
+            const WgradItem it = wgrad_item<NB>(item, e, tile_start, p);
             if (it.rows == 0) continue;
             const uint32_t n_kb = static_cast<uint32_t>((it.rows + 63) / 64);
             steps += n_kb;
             const int v = it.rows - static_cast<int>(n_kb - 1) * 64;
             if (!needs_clearing(v)) continue;
-            const uint32_t stage = (steps - 1) % kRwStages;
+            const uint32_t stage = (steps - 1) % kStages;
             const uint32_t phase = (phases >> stage) & 1u;
             phases ^= 1u << stage;
             if (!mbar_wait(&tail[stage], phase, timeout)) break;
-            const uint32_t sa = smem_u32(smem + stage * 2 * kRgOperand);
+            const uint32_t sa = smem_u32(smem + stage * C::kStage);
             const int lines = ((v + 15) & ~15) - v;  // 1..15 lines of 128 bytes per box
-            const int nbox = 2 + it.n_mma / 128;
-            for (int i = lane; i < nbox * lines * 8; i += 32) {
+            // every box of the stage (those not loaded for this item hold nothing that is used)
+            for (int i = lane; i < 2 * (1 + NB) * lines * 8; i += 32) {
                 const int box = i / (lines * 8), at = i - box * lines * 8;
                 sts128(sa + box * (kRgOperand / 2) + v * 128 + at * 16, make_uint4(0u, 0u, 0u, 0u));
             }
@@ -1131,46 +1231,94 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kRwThreads, 1)
             if (lane == 0) mbar_arrive_async(full_lead + 8u * stage);
         }
     } else if (warp >= 4) {
-        // ---------------- epilogue: lanes = rows n, two warps per quadrant share the product's columns
+        // ---------------- epilogue: lanes = rows n, two warps per quadrant share a product's columns
         const int q = warp & 3, sub = (warp - 4) / 4;
         const uint32_t acc_empty_lead = mapa_shared(smem_u32(acc_empty), 0);
-        const uint8_t *stage_ptr = smem + kRwOutOff + (warp - 4) * 2 * kRwStageOut;
-        uint32_t uses = 0, n_out = 0;
+        const uint32_t t0 = tmem_base + (static_cast<uint32_t>(q * 32) << 16);
+        WgradOut<C::kOutBufs> out{&tm_dw, smem + C::kOutOff + (warp - 4) * C::kOutBufs * kRwStageOut,
+                                  policy_evict_first(), 0u};
+        uint32_t uses = 0;
         bool ok = true;
-        for (int item = pair; item < total && ok; item += n_pairs) {
-            const WgradItem it = wgrad_item(item, tile_start, p);
+        for (int item = pair, e = 0; item < total && ok; item += n_pairs) {
+            const WgradItem it = wgrad_item<NB>(item, e, tile_start, p);
             const int n_kb = (it.rows + 63) / 64;
-            const int cols = it.n_mma / 2;  // this warp's columns: [cols sub, cols (sub + 1))
-            uint32_t acc[8][16];
-            if (n_kb == 0) {
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-#pragma unroll
-                    for (int j = 0; j < 16; ++j) acc[i][j] = 0u;
-            }
-            for (int kb = 0; kb < n_kb; kb += p.g.seg_kb, ++uses) {
-                if (!mbar_wait(&acc_full[uses & 1], (uses >> 1) & 1u, timeout)) {
-                    ok = false;
-                    break;
-                }
-                tc_fence_after();
-                const uint32_t t = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + (uses & 1) * 256 + cols * sub;
-                add_segment<false, 8>(t, 0, 16, cols, kb == 0, acc);
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive_async(acc_empty_lead + 8u * (uses & 1));
-            }
-            if (!ok) break;
             const int n = it.n0 + static_cast<int>(rank) * kBM + q * 32;
-            const int k = it.k0 + cols * sub, k_end = min(p.K, k + cols);
-            if (n < p.g.M) {  // warp-uniform
-                const uint32_t stage = smem_u32(stage_ptr);
+            const bool live = n < p.g.M;  // warp-uniform
+            if constexpr (NB == 1) {
+                const int cols = wgrad_cols(it.k0, p.K) / 2;  // this warp's columns: [cols sub, cols (sub + 1))
+                uint32_t acc[8][16];
+                if (n_kb == 0) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) acc[i][j] = 0u;
+                }
+                for (int kb = 0; kb < n_kb; kb += p.g.seg_kb, ++uses) {
+                    if (!mbar_wait(&acc_full[uses & 1], (uses >> 1) & 1u, timeout)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    add_segment<false, 8>(t0 + (uses & 1) * 256 + cols * sub, 0, 16, cols, kb == 0, acc);
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_async(acc_empty_lead + 8u * (uses & 1));
+                }
+                if (!ok) break;
+                const int k = it.k0 + cols * sub, k_end = min(p.K, k + cols);
+                if (live) {
+                    if (p.g.out_type == BEAM_MOE_BF16)
+                        wgrad_store<BEAM_MOE_BF16>(out, it.group, n, k, k_end, false, acc);
+                    else if (p.g.out_type == BEAM_MOE_F16)
+                        wgrad_store<BEAM_MOE_F16>(out, it.group, n, k, k_end, false, acc);
+                    else
+                        wgrad_store<BEAM_MOE_F32>(out, it.group, n, k, k_end, p.accumulate != 0, acc);
+                }
+            } else if (p.g.out_type == BEAM_MOE_F32) {
+                // one pass per segment (one without sums for a group without rows): store, or add
+                for (int kb = 0; kb == 0 || kb < n_kb; kb += p.g.seg_kb) {
+                    if (n_kb > 0) {
+                        ok = mbar_wait(acc_full, uses & 1u, timeout);
+                        if (!ok) break;
+                        tc_fence_after();
+                        if (kb > 0 && lane == 0) bulk_wait_all();  // this segment's adds follow the last one's stores
+                        __syncwarp();
+                    }
+#pragma unroll 1
+                    for (int b = 0; b < 2; ++b) {
+                        const int cols = wgrad_cols(it.k0 + 256 * b, p.K) / 2;
+                        const int k = it.k0 + 256 * b + cols * sub;
+#pragma unroll 1
+                        for (int c = 0; c < cols && k + c < p.K; c += 32) {
+                            uint32_t r[2][16] = {};
+                            if (n_kb > 0) {
+                                tmem_ld16(t0 + 256 * b + cols * sub + c, r[0]);
+                                tmem_ld16(t0 + 256 * b + cols * sub + c + 16, r[1]);
+                                tmem_ld_wait();
+                            }
+                            if (live)
+                                out.chunk(k + c, n, it.group, kb > 0 || p.accumulate != 0,
+                                          [&](int i) { return r[i / 16][i % 16]; });
+                        }
+                    }
+                    if (n_kb > 0) {
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive_async(acc_empty_lead);
+                        ++uses;
+                    }
+                }
+            } else {
+                if (n_kb > 0) {
+                    ok = mbar_wait(acc_full, uses & 1u, timeout);
+                    if (!ok) break;
+                    tc_fence_after();
+                    ++uses;
+                }
                 if (p.g.out_type == BEAM_MOE_BF16)
-                    wgrad_store<BEAM_MOE_BF16>(&tm_dw, it, n, k, k_end, 0, stage, stage_ptr, n_out, acc);
-                else if (p.g.out_type == BEAM_MOE_F16)
-                    wgrad_store<BEAM_MOE_F16>(&tm_dw, it, n, k, k_end, 0, stage, stage_ptr, n_out, acc);
+                    wgrad_pack_store<BEAM_MOE_BF16>(out, it, p.K, sub, n, live, n_kb > 0, t0, acc_empty_lead);
                 else
-                    wgrad_store<BEAM_MOE_F32>(&tm_dw, it, n, k, k_end, p.accumulate, stage, stage_ptr, n_out, acc);
+                    wgrad_pack_store<BEAM_MOE_F16>(out, it, p.K, sub, n, live, n_kb > 0, t0, acc_empty_lead);
             }
         }
         if (lane == 0) bulk_wait_all();

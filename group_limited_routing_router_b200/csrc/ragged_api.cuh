@@ -61,12 +61,13 @@ int init_ragged(int *dev_out) {
     RaggedDevice &d = g_ragged[*dev_out];
     const int sms = g_dev[*dev_out].num_sms;
     std::call_once(d.once, [&]() {
-        bool ok = set_pair_smem<1>() && set_pair_smem<2>() && set_smem(ragged_wgrad_kernel, kRwSmem) &&
+        bool ok = set_pair_smem<1>() && set_pair_smem<2>() && set_smem(ragged_wgrad_kernel<1>, RwgradCfg<1>::kSmem) &&
+                  set_smem(ragged_wgrad_kernel<2>, RwgradCfg<2>::kSmem) &&
                   set_split_smem<RS_FEW_ARGS>() && set_split_smem<RS_MID_ARGS>();
         if (ok) {
             // one CTA per SM in all variants
             d.pairs = max_clusters(ragged_pair_kernel<false, false, 1>, kRgThreads, RpairCfg<1>::kSmem, 2, sms);
-            d.wgrad_pairs = max_clusters(ragged_wgrad_kernel, kRwThreads, kRwSmem, 2, sms);
+            d.wgrad_pairs = max_clusters(ragged_wgrad_kernel<1>, kRwThreads, RwgradCfg<1>::kSmem, 2, sms);
             for (int i = 0; i < 4; ++i)  // both split kernels run one CTA per SM
                 d.clusters[i] = max_clusters(ragged_split_kernel<false, false, RS_MID_ARGS>, kRgThreads,
                                              RsplitCfg<RS_MID_ARGS>::kSmem, 1 << i, sms);
@@ -114,13 +115,19 @@ bool width_ok(int64_t w, int step) { return w >= step && w <= 65536 && w % step 
 bool ld_ok(int64_t ld, int64_t width, int esize) { return ld >= width && ld <= kMaxLd && (ld * esize) % 16 == 0; }
 bool aligned_to(const void *p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
-// k-steps per accumulation segment.  A segment's error is the tensor core's truncation, up to 4 instructions
-// per k-step x 2^-23 of the running sum: 16 steps stay below 2^-17, a sixteenth of fp16's half step, and 4
-// steps, for fp32 results, near 2^-20 of a partial sum that is itself a small part of the whole.
+// k-steps per accumulation segment.  Each instruction (16 products per sum; 4 to a k-step) truncates the
+// running sum, half of 2^-23 of it on average, always toward zero: a sum that grows evenly loses 2^-25 of its
+// end value per instruction, one of mixed signs far less (5120 products: 1.3e-6 in one segment, 2.3e-7 in
+// segments of 256).  fp32 results: 4 k-steps, 2^-21.  16-bit results: 16 k-steps, 2^-19.
 int segment_steps(bool i8, int out_type, int n_kb) {
     if (i8) return std::max(n_kb, 1);  // INT32 sums are exact
     return out_type == BEAM_MOE_F32 ? 4 : 16;
 }
+// The wide tiles sum 16-bit results in one segment where that loses at most an eighth of the result's half
+// step: length / 16 x 2^-25 <= 2^-12 (bf16) or 2^-15 (fp16).
+bool one_segment_ok(int dtype, int64_t length) { return length <= (dtype == BEAM_MOE_BF16 ? 131072 : 16384); }
+// wgrad's wide tiles flush fp32 results every 4096 rows: 256 instructions, 2^-17 at most.
+constexpr int kFlushSteps = 64;
 
 uint32_t ragged_idesc(bool i8, int dtype, int M, bool a_mn, bool b_mn) {
     uint32_t d = static_cast<uint32_t>(M >> 4) << 24;
@@ -248,7 +255,8 @@ int ragged_product(const RaggedCall &c, cudaStream_t s) {
     if (!encode_fn()) return BEAM_MOE_ERR_CUDA;
     const int kelems = kRgRowBytes / esize;
     const int n_kb = (width + kelems - 1) / kelems;
-    const RaggedPlan P = ragged_plan(d, c.E, c.R, M, n_kb, c.i8 || c.out_type != BEAM_MOE_F32);
+    const RaggedPlan P = ragged_plan(d, c.E, c.R, M, n_kb,
+                                     c.i8 || (c.out_type != BEAM_MOE_F32 && one_segment_ok(c.dtype, width)));
     RaggedParams p{};
     p.offsets = c.offsets;
     p.out = c.out;
@@ -284,6 +292,18 @@ int wgrad_splits(int E, int64_t R, int K, int N) {
     const int64_t tiles = static_cast<int64_t>(E) * ((N + 255) / 256) * ((K + 255) / 256);
     const int64_t by_rows = R / E / 512;
     return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(74 / tiles, by_rows), 64)));
+}
+// Whether wgrad's 256 x 512 tiles run: where their rounds come out shorter for a mean group, with the cycles
+// measured per k-step (~690 for 256 columns, ~1060 for 512, both bound by L2) and per item (decoding and
+// the hand-over; for 512 also its epilogue, which the products wait for).  bf16, 8 groups of 8192 rows: 1.17
+// against 1.65 ms, 64 of 256: 0.44 against 0.49, 64 of 128: 0.44 against 0.37; fp32, 64 of 256: 0.87 against 0.79.
+bool wgrad_wide(const RaggedDevice &d, int E, int64_t R, int K, int N, int splits, int dtype, int store) {
+    if (splits > 1 || K <= 256 || (store != BEAM_MOE_F32 && !one_segment_ok(dtype, R))) return false;
+    const int64_t n_kb = (R / E + 63) / 64, n_mt = (N + 255) / 256;
+    const int64_t rounds1 = (E * n_mt * ((K + 255) / 256) + d.wgrad_pairs - 1) / d.wgrad_pairs;
+    const int64_t rounds2 = (E * n_mt * ((K + 511) / 512) + d.wgrad_pairs - 1) / d.wgrad_pairs;
+    const int64_t epilogue = store == BEAM_MOE_F32 ? 7000 * ((n_kb + kFlushSteps - 1) / kFlushSteps) : 2500;
+    return rounds2 * (n_kb * 1060 + epilogue) < rounds1 * (n_kb * 690 + 700);
 }
 size_t wgrad_ws(int E, int64_t R, int K, int N) {
     const int s = R > 0 ? wgrad_splits(E, R, K, N) : 1;
@@ -403,12 +423,16 @@ int beam_moe_grouped_mm_wgrad(int32_t n_experts, int64_t R, int32_t K, int32_t N
     p.g.R = R;
     p.g.E = n_experts;
     p.g.M = N;
-    p.g.seg_kb = segment_steps(false, store, 0);
+    const bool wide = wgrad_wide(g_ragged[dev], n_experts, R, K, N, splits, dtype, store);
+    // NB = 2: 16-bit results in one segment, fp32 ones flushed
+    p.g.seg_kb = !wide ? segment_steps(false, store, 0) : (store == BEAM_MOE_F32 ? kFlushSteps : 1 << 30);
     p.g.out_type = store;
     p.g.idesc = ragged_idesc(false, dtype, kPairRows, true, true);
     p.g.timeout = kDefaultTimeoutCycles;
     p.K = K;
-    p.n_nt = (K + 255) / 256;
+    p.n_mt = (N + 255) / 256;
+    p.n_nt = wide ? (K + 511) / 512 : (K + 255) / 256;
+    p.nt_inv = static_cast<uint32_t>(((uint64_t(1) << 32) + p.n_nt - 1) / p.n_nt);  // n_nt = 1 is not divided by
     p.splits = splits;
     p.accumulate = splits > 1 ? 0 : (accumulate != 0);
     const CUtensorMapDataType dt = store == BEAM_MOE_F32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
@@ -419,8 +443,9 @@ int beam_moe_grouped_mm_wgrad(int32_t n_experts, int64_t R, int32_t K, int32_t N
         !map_groups(&m_dw, dt, type_size(store), splits > 1 ? ws : dw, K, N, static_cast<uint64_t>(splits) * n_experts,
                     128u / static_cast<uint32_t>(type_size(store)), 32))
         return BEAM_MOE_ERR_CUDA;
-    ragged_wgrad_kernel<<<static_cast<unsigned>(2 * g_ragged[dev].wgrad_pairs), kRwThreads, kRwSmem, s>>>(m_dy, m_x,
-                                                                                                         m_dw, p);
+    const unsigned wg = static_cast<unsigned>(2 * g_ragged[dev].wgrad_pairs);
+    if (wide) ragged_wgrad_kernel<2><<<wg, kRwThreads, RwgradCfg<2>::kSmem, s>>>(m_dy, m_x, m_dw, p);
+    else ragged_wgrad_kernel<1><<<wg, kRwThreads, RwgradCfg<1>::kSmem, s>>>(m_dy, m_x, m_dw, p);
     if ((rc = launch_status()) || splits == 1) return rc;
     const int64_t n4 = n / 4;
     const unsigned grid = static_cast<unsigned>(std::min<int64_t>((n4 + 255) / 256, 8 * g_dev[dev].num_sms));

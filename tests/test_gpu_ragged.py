@@ -1,10 +1,10 @@
 """Grouped matrix products, their gradients, the INT8 products and SwiGLU against plain 64-bit formulas.
 
 Tolerances, per element, from the number formats:
-  - a product's accumulation: within one segment each tensor-core instruction (16 products added to the
-    running sum) loses at most 17 units of 2^-25 of the largest magnitude involved, < 2^-20 of
-    S = sum |a||b|; a segment has at most 64 instructions (16 for fp32 results); segments, split and
-    join sums are FP32 additions, each within 2^-24 of S;
+  - a product's accumulation: each tensor-core instruction adds 16 products to the running FP32 sum and
+    truncates, which loses less than two units of its last place, 2^-22 of S = sum |a||b|; fp32 results
+    are flushed or cut at least every 256 instructions; segments, split and join sums are FP32 additions,
+    each within 2^-24 of S;
   - the result's rounding: half a step, torch.finfo(t).eps / 2 of its magnitude (and half the smallest
     subnormal of fp16).
 INT8 sums are exact; their scaling is three FP32 roundings.
@@ -48,9 +48,11 @@ def half_step(want, dtype):
 
 def sum_tol(mag, length, dtype):
     """Bound of the accumulation error of `length` products of summed magnitude `mag`."""
-    instructions = min(64 if dtype != F32 else 16, length // 16 + 1)
-    segments = length // (64 * 16 if dtype != F32 else 64 * 4) + 1
-    return mag * (instructions * 2.0 ** -20 + (segments + 72) * 2.0 ** -24)
+    instructions = length // 16 + 1
+    if dtype == F32:
+        instructions = min(instructions, 256)
+    segments = length // 256 + 1  # the shortest cut, of fp32 results: 256 products
+    return mag * (instructions * 2.0 ** -22 + (segments + 72) * 2.0 ** -24)
 
 
 def check(got, want, tol, what):
