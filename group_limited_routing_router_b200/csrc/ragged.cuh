@@ -86,30 +86,10 @@ __device__ __forceinline__ uint32_t idesc_with_n(uint32_t idesc, int n) {
 }
 
 // Arrives on a barrier of either CTA of the pair.  What is handed over is TMEM, ordered by the tcgen05 fences
-// on both sides, or this CTA's shared memory after a proxy fence: no other memory operation has to be
-// performed first, which a release at cluster scope would wait for.
+// on both sides, or this CTA's shared memory, after a proxy fence or to be overwritten: no other memory
+// operation has to be performed first, which a release at cluster scope would wait for.
 __device__ __forceinline__ void mbar_arrive_async(uint32_t bar_cluster) {
     asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar_cluster) : "memory");
-}
-
-// mbar_wait whose acquire covers the other CTAs of the cluster (they arrive with release.cluster).
-__device__ __forceinline__ bool mbar_wait_cluster(uint64_t *bar, uint32_t parity, long long timeout) {
-    const long long t0 = clock64();
-    while (true) {
-        uint32_t ok;
-        asm volatile(
-            "{\n\t.reg .pred p;\n\t"
-            "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
-            "selp.u32 %0, 1, 0, p;\n\t}\n"
-            : "=r"(ok)
-            : "r"(smem_u32(bar)), "r"(parity), "r"(kWaitSuspendNs)
-            : "memory");
-        if (ok) return true;
-        if (clock64() - t0 > timeout) {
-            set_status(BEAM_MOE_ERR_DEVICE_TIMEOUT);
-            return false;
-        }
-    }
 }
 
 // ---- groups --------------------------------------------------------------------------------------
@@ -169,20 +149,23 @@ __device__ __forceinline__ int find_group(int item, const int *tile_start, int E
     return lo;
 }
 
-// Forward / dgrad item: feature tile mt, row tile of group e.
+// Forward / dgrad item: feature tile mt, row tile of group e.  The items a role decodes ascend: `e` starts at
+// the first one's group (find_group) and walks along.
 struct RaggedItem {
     int e, mt, n_valid, n_mma;
     int once;  // the group has one row tile, so its weights are read once: L2 evict-first
     int64_t row0;
 };
 template <int BN, int ROUND>
-__device__ __forceinline__ RaggedItem ragged_item(int item, const int *tile_start, const RaggedParams &p) {
+__device__ __forceinline__ RaggedItem ragged_item(int item, int &e, const int *tile_start, const RaggedParams &p) {
     RaggedItem it;
-    it.e = find_group(item, tile_start, p.E);
-    const int rows = group_rows(p, it.e);
-    const int n_nt = (rows + BN - 1) / BN, per = tile_rows<BN, ROUND>(rows);
-    const int local = item - tile_start[it.e];
-    it.mt = local / n_nt;
+    while (tile_start[e + 1] <= item) ++e;
+    it.e = e;
+    const int rows = group_rows(p, e);
+    const int n_nt = (rows + BN - 1) / BN;
+    const int per = n_nt == 1 ? (rows + ROUND - 1) / ROUND * ROUND : tile_rows<BN, ROUND>(rows);
+    const int local = item - tile_start[e];
+    it.mt = n_nt == 1 ? local : local / n_nt;
     const int nt = local - it.mt * n_nt;
     it.n_valid = min(per, rows - nt * per);  // > 0: rows > BN (n_nt - 1) >= per (n_nt - 1)
     it.n_mma = (it.n_valid + ROUND - 1) / ROUND * ROUND;
@@ -421,7 +404,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kRgThreads, 1)
     cluster_sync_all();
     tc_fence_after();
     const uint32_t tmem_base = *tmem_slot;
-    const int total = tile_start[p.E];
+    const int total = tile_start[p.E], first = find_group(pair, tile_start, p.E);
 
     if (warp == 0) {
         if (lane == 0) {
@@ -433,8 +416,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kRgThreads, 1)
             int stage = 0;
             uint32_t phase = 0, issued = 0, issued_phase = 0;
             bool ok = true;
-            for (int item = pair; item < total && ok; item += n_pairs) {
-                const RaggedItem it = ragged_item<kRpBN, kRound>(item, tile_start, p);
+            for (int item = pair, e = first; item < total && ok; item += n_pairs) {
+                const RaggedItem it = ragged_item<kRpBN, kRound>(item, e, tile_start, p);
                 const uint64_t pol_w = it.once ? pol_once : pol_again;
                 const int half = it.n_mma / 2;
                 const int nbox = (half + kRpBox - 1) / kRpBox;
@@ -481,8 +464,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kRgThreads, 1)
             int stage = 0;
             uint32_t phase = 0, uses = 0;
             bool ok = true;
-            for (int item = pair; item < total && ok; item += n_pairs) {
-                const RaggedItem it = ragged_item<kRpBN, kRound>(item, tile_start, p);
+            for (int item = pair, e = first; item < total && ok; item += n_pairs) {
+                const RaggedItem it = ragged_item<kRpBN, kRound>(item, e, tile_start, p);
                 const uint32_t idesc = idesc_with_n(p.idesc, it.n_mma);
                 for (int kb = 0; kb < p.n_kb && ok;) {
                     const int seg_end = NA == 1 ? min(p.n_kb, kb + p.seg_kb) : p.n_kb;
@@ -493,7 +476,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kRgThreads, 1)
                     }
                     tc_fence_after();
                     const uint32_t d = tmem_base + slot * 256;
-                    for (bool first = true; kb < seg_end; ++kb, first = false) {
+                    for (bool start = true; kb < seg_end; ++kb, start = false) {
                         if (!mbar_wait(&full[stage], phase, p.timeout)) {
                             ok = false;
                             break;
@@ -503,7 +486,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kRgThreads, 1)
                         const uint64_t db = umma_desc_sw128(sa + NA * kRgOperand);
 #pragma unroll
                         for (int kk = 0; kk < 4; ++kk) {  // 32 bytes of the contraction per instruction
-                            const uint32_t accum = (!first || kk > 0) ? 1u : 0u;
+                            const uint32_t accum = (!start || kk > 0) ? 1u : 0u;
 #pragma unroll
                             for (int a = 0; a < NA; ++a) {
                                 const uint32_t at = sa + a * kRgOperand;
@@ -533,8 +516,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kRgThreads, 1)
         const uint32_t t0 = tmem_base + (static_cast<uint32_t>(q * 32) << 16);
         uint32_t uses = 0;
         bool ok = true;
-        for (int item = pair; item < total && ok; item += n_pairs) {
-            const RaggedItem it = ragged_item<kRpBN, kRound>(item, tile_start, p);
+        for (int item = pair, e = first; item < total && ok; item += n_pairs) {
+            const RaggedItem it = ragged_item<kRpBN, kRound>(item, e, tile_start, p);
             const int m = it.mt * NA * kPairRows + static_cast<int>(rank) * kBM + q * 32 + lane;
             if constexpr (NA == 1) {
                 uint32_t acc[kRpBN / 32][16];
@@ -584,8 +567,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kRgThreads, 1)
 // sums of its features in rank order (so results do not depend on timing) and stores them.
 template <int BN, int STAGES>
 struct RsplitCfg {
+    static constexpr int kBox = BN == 32 ? 16 : 64;  // rows per B box (a box costs its producer as much as its bytes)
     static constexpr int kStage = kRgOperand + BN * kRgRowBytes;
-    static constexpr int kRedOff = STAGES * kStage;           // [S][BN][128 / S] fp32 (INT8: int32)
+    static constexpr int kRedOff = STAGES * kStage;           // the partial sums, fp32 (INT8: int32): partial_at
     static constexpr int kBarOff = kRedOff + BN * kBM * 4;
     static constexpr int kTileOff = kBarOff + 256;
     static constexpr int kSmem = 1024 + kTileOff + 4 * (kPmMaxE + 1) + 64;
@@ -593,54 +577,79 @@ struct RsplitCfg {
     static_assert(8 * (2 * STAGES + 4 + 2 + 1) + 4 <= 256, "barrier area");
     static_assert(kStage % 1024 == 0 && kSmem + 128 <= 232448, "shared memory per CTA");
 };
-constexpr int kRsBox = 16;  // rows per B box
-
-__device__ __forceinline__ void st_cluster_u32(uint32_t addr, uint32_t v) {
-    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+// 16 bytes to shared memory of a CTA of the cluster; they complete on an mbarrier of that CTA, so neither side
+// needs a fence (plain remote stores with a cluster-scope release took about 3 us per item).
+__device__ __forceinline__ void st_async_v4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d,
+                                            uint32_t bar) {
+    asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.u32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(addr),
+                 "r"(a), "r"(b), "r"(c), "r"(d), "r"(bar)
+                 : "memory");
 }
-__device__ __forceinline__ void fence_cluster() { asm volatile("fence.acq_rel.cluster;" ::: "memory"); }
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+// Partial sums in a CTA's shared memory: [S][F = 128 / S features][BN rows], four rows (16 bytes) at a time,
+// those of feature f at place (rows / 4) ^ (f & 7), so that neighbouring features fall into different banks.
+template <int BN>
+__device__ __forceinline__ uint32_t partial_at(uint32_t feature, uint32_t quad) {
+    return feature * (BN * 4) + ((quad ^ (feature & 7u)) << 4);
+}
 
-// This CTA's features of one item: the S partial sums of two neighbouring features per thread, added in
-// rank order, stored as pairs.  buf: [S][BN][F] in this CTA's shared memory, F = 128 / S.
+// This CTA's features (m0 ..) of one item: the S partial sums of four rows of a feature per thread and step, added
+// in rank order; 16-bit results are paired with the neighbouring lane's feature.
 template <bool I8, int BN, int TYPE>
-__device__ __forceinline__ void reduce_store(const RaggedParams &p, const RaggedItem &it, const float *buf, int S, int F,
+__device__ __forceinline__ void reduce_store(const RaggedParams &p, const RaggedItem &it, uint32_t buf, int S, int F,
                                              int m0, int tid) {
-    const int pairs = F / 2;
-    for (int idx = tid; idx < it.n_valid * pairs; idx += 32 * kGemmEpiWarps) {
-        const int row = idx / pairs, f = 2 * (idx - row * pairs);
-        const int m = m0 + f;
-        if (m >= p.M) continue;
-        float a = 0.0f, b = 0.0f;
-        if constexpr (I8) {
-            int32_t ia = 0, ib = 0;
-            for (int s = 0; s < S; ++s) {
-                const int2 v = *reinterpret_cast<const int2 *>(buf + (s * BN + row) * F + f);
-                ia += v.x;
-                ib += v.y;
+    const int log_f = 31 - __clz(F);
+    const int total = ((it.n_valid + 3) >> 2) << log_f;  // four-row pieces
+    const int f = tid & (F - 1), m = m0 + f;             // F divides 256: a thread keeps its feature
+    const float channel = (I8 && m < p.M) ? __ldg(p.channel_scale + static_cast<int64_t>(it.e) * p.M + m) : 1.0f;
+    for (int idx = tid; idx - (tid & 31) < total; idx += 32 * kGemmEpiWarps) {  // warp-uniform
+        const int quad = idx >> log_f;
+        const bool live = idx < total && m < p.M;
+        float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        if (live) {
+            uint4 sum = lds128(buf + partial_at<BN>(f, quad));
+            for (int s = 1; s < S; ++s) {
+                const uint4 u = lds128(buf + partial_at<BN>(s * F + f, quad));
+                if constexpr (I8) {
+                    sum = make_uint4(sum.x + u.x, sum.y + u.y, sum.z + u.z, sum.w + u.w);
+                } else {
+                    sum = make_uint4(__float_as_uint(__uint_as_float(sum.x) + __uint_as_float(u.x)),
+                                     __float_as_uint(__uint_as_float(sum.y) + __uint_as_float(u.y)),
+                                     __float_as_uint(__uint_as_float(sum.z) + __uint_as_float(u.z)),
+                                     __float_as_uint(__uint_as_float(sum.w) + __uint_as_float(u.w)));
+                }
             }
-            const float rs = __ldg(p.row_scale + it.row0 + row);
-            const float *cs = p.channel_scale + static_cast<int64_t>(it.e) * p.M + m;
-            a = static_cast<float>(ia) * (__ldg(cs) * rs);
-            b = static_cast<float>(ib) * (__ldg(cs + 1) * rs);
-        } else {
-            for (int s = 0; s < S; ++s) {
-                const float2 v = *reinterpret_cast<const float2 *>(buf + (s * BN + row) * F + f);
-                a += v.x;
-                b += v.y;
+            const uint32_t w[4] = {sum.x, sum.y, sum.z, sum.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float row = (I8 && 4 * quad + j < it.n_valid) ? __ldg(p.row_scale + it.row0 + 4 * quad + j) : 1.0f;
+                v[j] = ragged_value<I8>(p, w[j], channel, row);
             }
         }
-        const int64_t at = (it.row0 + row) * p.ldo + m;
-        if constexpr (TYPE == BEAM_MOE_F32)
-            *reinterpret_cast<float2 *>(reinterpret_cast<float *>(p.out) + at) = make_float2(a, b);
-        else
-            *reinterpret_cast<uint32_t *>(reinterpret_cast<uint16_t *>(p.out) + at) = pack2<TYPE>(a, b);
+        const int left = live ? it.n_valid - 4 * quad : 0;
+        if constexpr (TYPE == BEAM_MOE_F32) {
+            float *o = reinterpret_cast<float *>(p.out) + (it.row0 + 4 * quad) * p.ldo + m;
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (j < left) o[j * p.ldo] = v[j];
+        } else {
+            const int odd = tid & 1;
+            uint16_t *o = reinterpret_cast<uint16_t *>(p.out) + (it.row0 + 4 * quad + odd) * p.ldo + (m & ~1);
+#pragma unroll
+            for (int j = 0; j < 4; j += 2) {
+                const float got = __shfl_xor_sync(0xffffffffu, odd ? v[j] : v[j + 1], 1);
+                const uint32_t pr = odd ? pack2<TYPE>(got, v[j + 1]) : pack2<TYPE>(v[j], got);
+                if (j + odd < left) *reinterpret_cast<uint32_t *>(o + j * p.ldo) = pr;
+            }
+        }
     }
 }
 
 template <bool I8, bool A_MN, int BN, int STAGES>
 __global__ void __launch_bounds__(kRgThreads, 1)
     ragged_split_kernel(const __grid_constant__ CUtensorMap tm_w,  // weights [E][N][K]
-                        const __grid_constant__ CUtensorMap tm_b,  // rows [R][contraction], kRsBox-row box
+                        const __grid_constant__ CUtensorMap tm_b,  // rows [R][contraction], kBox-row box
                         const RaggedParams p) {
     using C = RsplitCfg<BN, STAGES>;
     constexpr int kChunks = (BN + 31) / 32;
@@ -674,7 +683,7 @@ __global__ void __launch_bounds__(kRgThreads, 1)
             mbar_init(&acc_full[a], 1);
             mbar_init(&acc_empty[a], kGemmEpiWarps);
         }
-        mbar_init(red_full, kGemmEpiWarps * S);
+        mbar_init(red_full, 1);
         mbar_init(red_empty, kGemmEpiWarps * S);
         mbar_init(drain, 1);
         fence_mbar_init();
@@ -688,10 +697,10 @@ __global__ void __launch_bounds__(kRgThreads, 1)
     ragged_prefix<BN, false>(p, n_mt, false, tile_start);
     tc_fence_before();
     __syncthreads();
-    cluster_sync_all();  // every CTA's barriers are initialised before another one signals them
+    cluster_arrive();  // the epilogue waits for the other CTAs' barriers before it signals them; nobody else does
     tc_fence_after();
     const uint32_t tmem_base = *tmem_slot;
-    const int total = tile_start[p.E];
+    const int total = tile_start[p.E], first = find_group(cluster, tile_start, p.E);
 
     if (warp == 0) {
         if (lane == 0) {
@@ -701,12 +710,12 @@ __global__ void __launch_bounds__(kRgThreads, 1)
             int stage = 0;
             uint32_t phase = 0, issued = 0, issued_phase = 0;
             bool ok = true;
-            for (int item = cluster; item < total && ok; item += n_clusters) {
-                const RaggedItem it = ragged_item<BN, 16>(item, tile_start, p);
+            for (int item = cluster, e = first; item < total && ok; item += n_clusters) {
+                const RaggedItem it = ragged_item<BN, 16>(item, e, tile_start, p);
                 const uint64_t pol_w = it.once ? pol_once : pol_again;
-                const int nbox = it.n_mma / kRsBox;
+                const int nbox = (it.n_mma + C::kBox - 1) / C::kBox;
                 const int a_row = it.mt * kBM;
-                const uint32_t bytes = static_cast<uint32_t>(kRgOperand + nbox * kRsBox * kRgRowBytes);
+                const uint32_t bytes = static_cast<uint32_t>(kRgOperand + nbox * C::kBox * kRgRowBytes);
                 for (int kb = kb0; kb < kb1; ++kb) {
                     if (!mbar_wait(&empty[stage], phase ^ 1u, p.timeout)) {
                         ok = false;
@@ -721,8 +730,8 @@ __global__ void __launch_bounds__(kRgThreads, 1)
                         tma_load_3d(sa, &tm_w, &full[stage], kb * kElems, a_row, it.e, pol_w);
                     }
                     for (int b = 0; b < nbox; ++b)
-                        tma_load_2d(sa + kRgOperand + b * kRsBox * kRgRowBytes, &tm_b, &full[stage], kb * kElems,
-                                    static_cast<int>(it.row0) + b * kRsBox, pol_x);
+                        tma_load_2d(sa + kRgOperand + b * C::kBox * kRgRowBytes, &tm_b, &full[stage], kb * kElems,
+                                    static_cast<int>(it.row0) + b * C::kBox, pol_x);
                     issued |= 1u << stage;
                     issued_phase = (issued_phase & ~(1u << stage)) | (phase << stage);
                     if (++stage == STAGES) {
@@ -739,8 +748,8 @@ __global__ void __launch_bounds__(kRgThreads, 1)
             int stage = 0;
             uint32_t phase = 0, uses = 0;
             bool ok = true;
-            for (int item = cluster; item < total && ok; item += n_clusters) {
-                const RaggedItem it = ragged_item<BN, 16>(item, tile_start, p);
+            for (int item = cluster, e = first; item < total && ok; item += n_clusters) {
+                const RaggedItem it = ragged_item<BN, 16>(item, e, tile_start, p);
                 const uint32_t idesc = idesc_with_n(p.idesc, it.n_mma);
                 for (int kb = kb0; kb < kb1 && ok;) {
                     const int seg_end = min(kb1, kb + p.seg_kb);
@@ -750,7 +759,7 @@ __global__ void __launch_bounds__(kRgThreads, 1)
                     }
                     tc_fence_after();
                     const uint32_t d = tmem_base + (uses & 1) * C::kSlot;
-                    for (bool first = true; kb < seg_end; ++kb, first = false) {
+                    for (bool start = true; kb < seg_end; ++kb, start = false) {
                         if (!mbar_wait(&full[stage], phase, p.timeout)) {
                             ok = false;
                             break;
@@ -761,7 +770,7 @@ __global__ void __launch_bounds__(kRgThreads, 1)
                         const uint64_t db = umma_desc_sw128(sa + kRgOperand);
 #pragma unroll
                         for (int kk = 0; kk < 4; ++kk) {
-                            const uint32_t accum = (!first || kk > 0) ? 1u : 0u;
+                            const uint32_t accum = (!start || kk > 0) ? 1u : 0u;
                             if (I8) umma_i8(d, da + 2 * kk, db + 2 * kk, idesc, accum);
                             else umma_bf16(d, da + (A_MN ? 128 : 2) * kk, db + 2 * kk, idesc, accum);
                         }
@@ -782,15 +791,15 @@ __global__ void __launch_bounds__(kRgThreads, 1)
     } else {
         const int q = warp & 3, sub = (warp - 2) / 4;
         const int F = kBM / static_cast<int>(S);
-        const float *buf = reinterpret_cast<const float *>(smem + C::kRedOff);
+        const uint32_t buf = smem_u32(smem + C::kRedOff);
         // this thread's feature q * 32 + lane belongs to CTA `dst`, which keeps it at index f of its F
         const uint32_t dst = static_cast<uint32_t>(q * 32 + lane) / F;
-        const uint32_t f = static_cast<uint32_t>(q * 32 + lane) % F;
-        const uint32_t push = mapa_shared(smem_u32(buf), dst) + 4u * (rank * BN * F + f);
+        const uint32_t f = rank * F + static_cast<uint32_t>(q * 32 + lane) % F;
+        const uint32_t push = mapa_shared(buf, dst), push_bar = mapa_shared(smem_u32(red_full), dst);
         uint32_t uses = 0, n_item = 0;
-        bool ok = true;
-        for (int item = cluster; item < total && ok; item += n_clusters, ++n_item) {
-            const RaggedItem it = ragged_item<BN, 16>(item, tile_start, p);
+        bool ok = true, joined = false;  // joined: the other CTAs' barriers are known to be initialised
+        for (int item = cluster, e = first; item < total && ok; item += n_clusters, ++n_item) {
+            const RaggedItem it = ragged_item<BN, 16>(item, e, tile_start, p);
             uint32_t acc[kChunks][16];
             for (int kb = kb0; kb < kb1; kb += p.seg_kb, ++uses) {
                 if (!mbar_wait(&acc_full[uses & 1], (uses >> 1) & 1u, p.timeout)) {
@@ -804,34 +813,47 @@ __global__ void __launch_bounds__(kRgThreads, 1)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&acc_empty[uses & 1]);
             }
+            if (!ok) break;
+            if (S == 1) {
+                const int m = it.mt * kBM + q * 32 + lane;
+                if (p.out_type == BEAM_MOE_BF16) store_item<I8, BEAM_MOE_BF16, kChunks>(p, it, sub, m, acc);
+                else if (p.out_type == BEAM_MOE_F16) store_item<I8, BEAM_MOE_F16, kChunks>(p, it, sub, m, acc);
+                else store_item<I8, BEAM_MOE_F32, kChunks>(p, it, sub, m, acc);
+                continue;
+            }
+            if (!joined) {
+                cluster_wait();
+                joined = true;
+            }
+            if (threadIdx.x == 64)  // what the S CTAs push here for this item
+                mbar_arrive_expect_tx(red_full, static_cast<uint32_t>(kBM * ((it.n_valid + 3) >> 2) * 16));
             // the last item's partial sums have been read everywhere, then these are pushed
-            ok = ok && mbar_wait_cluster(red_empty, (n_item & 1u) ^ 1u, p.timeout);
+            ok = mbar_wait(red_empty, (n_item & 1u) ^ 1u, p.timeout);
             if (!ok) break;
 #pragma unroll
             for (int i = 0; i < kChunks; ++i) {
                 const int c = 16 * sub + 32 * i;
 #pragma unroll
-                for (int j = 0; j < 16; ++j)
-                    if (c + j < it.n_valid) st_cluster_u32(push + 4u * static_cast<uint32_t>((c + j) * F), acc[i][j]);
+                for (int j = 0; j < 16; j += 4)
+                    if (c + j < it.n_valid)
+                        st_async_v4(push + partial_at<BN>(f, static_cast<uint32_t>(c + j) >> 2), acc[i][j],
+                                    acc[i][j + 1], acc[i][j + 2], acc[i][j + 3], push_bar);
             }
-            fence_cluster();
-            __syncwarp();
-            if (lane < static_cast<int>(S)) mbar_arrive_cluster(mapa_shared(smem_u32(red_full), lane));
-            if (!mbar_wait_cluster(red_full, n_item & 1u, p.timeout)) {
-                ok = false;
-                break;
-            }
+            ok = mbar_wait(red_full, n_item & 1u, p.timeout);
+            if (!ok) break;
             const int tid = static_cast<int>(threadIdx.x) - 64;
             const int m0 = it.mt * kBM + static_cast<int>(rank) * F;
             if (p.out_type == BEAM_MOE_BF16) reduce_store<I8, BN, BEAM_MOE_BF16>(p, it, buf, S, F, m0, tid);
             else if (p.out_type == BEAM_MOE_F16) reduce_store<I8, BN, BEAM_MOE_F16>(p, it, buf, S, F, m0, tid);
             else reduce_store<I8, BN, BEAM_MOE_F32>(p, it, buf, S, F, m0, tid);
-            fence_cluster();
-            __syncwarp();
-            if (lane < static_cast<int>(S)) mbar_arrive_cluster(mapa_shared(smem_u32(red_empty), lane));
+            __syncwarp();  // this warp has read its sums: one arrival per CTA of the cluster
+            if (item + n_clusters < total && lane < static_cast<int>(S))
+                mbar_arrive_async(mapa_shared(smem_u32(red_empty), lane));
         }
+        if (!joined) cluster_wait();
     }
     __syncwarp();
+    if (warp < 2) cluster_wait();
     tc_fence_before();
     __syncthreads();
     cluster_sync_all();  // no CTA leaves while another may still push to it or signal it
@@ -890,9 +912,8 @@ struct WgradParams {
     int accumulate;  // FP32 output: add to it, groups without rows are left alone
 };
 
-// Item `item` (of ascending ones; `e` walks along).  Every role decodes every item, and a short group's item
-// is over in ~2000 cycles: no search from the start and no slow division here (with both, 64 groups of 32
-// rows took 320 us instead of 250).
+// Every role decodes every item, and a short group's item is over in ~2000 cycles: no search from the start and
+// no slow division here (with both, 64 groups of 32 rows took 250 us without their stores instead of 135).
 template <int NB>
 __device__ __forceinline__ WgradItem wgrad_item(int item, int &e, const int *tile_start, const WgradParams &p) {
     WgradItem it;
@@ -1091,7 +1112,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kRwThreads, 1)
     cluster_sync_all();
     tc_fence_after();
     const uint32_t tmem_base = *tmem_slot;
-    const int total = tile_start[p.g.E];
+    const int total = tile_start[p.g.E], first = find_group(pair, tile_start, p.g.E);
 
     if (warp == 0) {
         if (lane == 0) {
@@ -1102,7 +1123,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kRwThreads, 1)
             int stage = 0;
             uint32_t phase = 0, issued = 0, issued_phase = 0;
             bool ok = true;
-            for (int item = pair, e = 0; item < total && ok; item += n_pairs) {
+            for (int item = pair, e = first; item < total && ok; item += n_pairs) {
                 const WgradItem it = wgrad_item<NB>(item, e, tile_start, p);
                 const int a_col = it.n0 + static_cast<int>(rank) * kBM;
                 int nbox[NB], b_col[NB];  // 64-column boxes of x per CTA
@@ -1154,7 +1175,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kRwThreads, 1)
             int stage = 0;
             uint32_t phase = 0, uses = 0;
             bool ok = true;
-            for (int item = pair, e = 0; item < total && ok; item += n_pairs) {
+            for (int item = pair, e = first; item < total && ok; item += n_pairs) {
                 const WgradItem it = wgrad_item<NB>(item, e, tile_start, p);
                 uint32_t idesc[NB];
                 int n_b = 0;  // products of the item
@@ -1174,7 +1195,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kRwThreads, 1)
                     }
                     tc_fence_after();
                     const uint32_t d = tmem_base + slot * 256;
-                    for (bool first = true; kb < seg_end; ++kb, first = false) {
+                    for (bool start = true; kb < seg_end; ++kb, start = false) {
                         if (!mbar_wait(&full[stage], phase, timeout)) {
                             ok = false;
                             break;
@@ -1189,7 +1210,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kRwThreads, 1)
                                 if (j < n_b)
                                     umma_bf16_pair(d + 256 * j, da + 128 * kk,
                                                    umma_desc_mn_sw128(sa + (1 + j) * kRgOperand) + 128 * kk, idesc[j],
-                                                   (!first || kk > 0) ? 1u : 0u);
+                                                   (!start || kk > 0) ? 1u : 0u);
                         umma_commit_pair_both(&empty[stage]);
                         if (++stage == kStages) {
                             stage = 0;
@@ -1208,7 +1229,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kRwThreads, 1)
         // ---------------- helper: clears the rows behind the group in its last k-step
         const uint32_t full_lead = mapa_shared(smem_u32(full), 0);
         uint32_t steps = 0, phases = 0;  // k-steps up to this item's end; per stage, the phase of `tail`
-        for (int item = pair, e = 0; item < total; item += n_pairs) {
+        for (int item = pair, e = first; item < total; item += n_pairs) {
             const WgradItem it = wgrad_item<NB>(item, e, tile_start, p);
             if (it.rows == 0) continue;
             const uint32_t n_kb = static_cast<uint32_t>((it.rows + 63) / 64);
@@ -1239,7 +1260,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kRwThreads, 1)
                                   policy_evict_first(), 0u};
         uint32_t uses = 0;
         bool ok = true;
-        for (int item = pair, e = 0; item < total && ok; item += n_pairs) {
+        for (int item = pair, e = first; item < total && ok; item += n_pairs) {
             const WgradItem it = wgrad_item<NB>(item, e, tile_start, p);
             const int n_kb = (it.rows + 63) / 64;
             const int n = it.n0 + static_cast<int>(rank) * kBM + q * 32;

@@ -209,8 +209,11 @@ RaggedPlan ragged_plan(const RaggedDevice &d, int E, int64_t R, int M, int n_kb,
     for (int i = 0; i < 4; ++i) {
         const int S = 1 << i;
         if (S > n_kb) break;
-        // rounds over the co-resident clusters x (k-steps per CTA + a fixed cost per item of ~4 steps)
-        const int64_t t = ((items + d.clusters[i] - 1) / d.clusters[i]) * ((n_kb + S - 1) / S + 4);
+        // rounds over the co-resident clusters x (k-steps per CTA + the item's fixed cost in k-steps of ~0.37 us:
+        // ~4, and for the exchange of the partial sums 1.2 us for 16 rows, 6 us for 128)
+        const int64_t rows = std::min<int64_t>(mean, bn);
+        const int64_t t = ((items + d.clusters[i] - 1) / d.clusters[i]) *
+                          ((n_kb + S - 1) / S + 4 + (S > 1 ? rows / 8 : 0));
         if (i == 0 || t < best) {
             best = t;
             P.S = S;
@@ -271,11 +274,12 @@ int ragged_product(const RaggedCall &c, cudaStream_t s) {
     p.row_scale = c.row_scale;
     p.channel_scale = c.channel_scale;
     p.timeout = kDefaultTimeoutCycles;
+    const int box = P.pair ? kRpBox : (P.few ? RsplitCfg<RS_FEW_ARGS>::kBox : RsplitCfg<RS_MID_ARGS>::kBox);
     CUtensorMap m_w, m_b;
     // dgrad's weight tile is 64 features (K, contiguous) by 64 contraction rows (N), two boxes per 128 features
     if (!map_groups(&m_w, esize == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, esize, c.w,
                     c.K, c.N, c.E, static_cast<uint32_t>(kelems), c.dgrad ? 64 : kBM) ||
-        !map_rows(&m_b, esize, c.rows, width, c.ld_rows, c.R, static_cast<uint32_t>(kelems), P.pair ? kRpBox : kRsBox))
+        !map_rows(&m_b, esize, c.rows, width, c.ld_rows, c.R, static_cast<uint32_t>(kelems), static_cast<uint32_t>(box)))
         return BEAM_MOE_ERR_CUDA;
     if (P.pair)
         return P.pair == 1 ? launch_pair<1>(c.i8, c.dgrad, d.pairs, s, m_w, m_b, p)
