@@ -226,7 +226,13 @@ __device__ __forceinline__ float ragged_value(const RaggedParams &p, uint32_t ac
 //     the accumulators to 16 bits in registers, hands TMEM back and then stores; fp32 results (of INT8 only:
 //     16-bit operands keep their short segments there) are stored chunk by chunk before TMEM goes back.
 constexpr int kRpBN = 256;
-constexpr int kRpBox = 32;  // rows per B box
+// The rows of a k-step come in one box, of the height among eight (16, 32 .. 128 rows) that holds a CTA's half of
+// the item's rows best: several small boxes cost more than their bytes (256 groups of 128 +- 11 rows, 5120 x 2560, NA = 1: 1.42 ms
+// in boxes of 32 rows, 1.48 with a remainder of 8-row boxes, 1.32 so).
+constexpr int kRpBoxStep = 16, kRpBoxes = 8;
+struct RowMaps {
+    CUtensorMap m[kRpBoxes];
+};
 template <int NA>
 struct RpairCfg {
     static constexpr int kStages = NA == 1 ? 7 : 4;
@@ -360,7 +366,7 @@ __device__ __forceinline__ void store_packed(const RaggedParams &p, const Ragged
 template <bool I8, bool A_MN, int NA>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kRgThreads, 1)
     ragged_pair_kernel(const __grid_constant__ CUtensorMap tm_w,  // weights [E][N][K]
-                       const __grid_constant__ CUtensorMap tm_b,  // rows [R][contraction], kRpBox-row box
+                       const __grid_constant__ RowMaps tm_b,      // rows [R][contraction], by box height
                        const RaggedParams p) {
     using C = RpairCfg<NA>;
     constexpr int kRound = I8 ? 32 : 16;
@@ -392,7 +398,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kRgThreads, 1)
         mbar_init(drain, 1);
         fence_mbar_init();
         prefetch_tensormap(&tm_w);
-        prefetch_tensormap(&tm_b);
     }
     if (warp == 1) {
         tmem_alloc_pair(tmem_slot, 512);
@@ -420,10 +425,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kRgThreads, 1)
                 const RaggedItem it = ragged_item<kRpBN, kRound>(item, e, tile_start, p);
                 const uint64_t pol_w = it.once ? pol_once : pol_again;
                 const int half = it.n_mma / 2;
-                const int nbox = (half + kRpBox - 1) / kRpBox;
+                const int box = (half + kRpBoxStep - 1) / kRpBoxStep;  // 1..8
+                const CUtensorMap *map_b = &tm_b.m[box - 1];
                 const int b_row = static_cast<int>(it.row0) + static_cast<int>(rank) * half;
                 const int a_row = it.mt * NA * kPairRows + static_cast<int>(rank) * kBM;
-                const uint32_t pair_bytes = 2u * static_cast<uint32_t>(NA * kRgOperand + nbox * kRpBox * kRgRowBytes);
+                const uint32_t pair_bytes = 2u * static_cast<uint32_t>(NA * kRgOperand + box * kRpBoxStep * kRgRowBytes);
                 for (int kb = 0; kb < p.n_kb; ++kb) {
                     if (!mbar_wait(&empty[stage], phase ^ 1u, p.timeout)) {
                         ok = false;
@@ -443,9 +449,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kRgThreads, 1)
                             tma_load_3d_pair(dst, &tm_w, bar, kb * kElems, row, it.e, pol_w);
                         }
                     }
-                    for (int b = 0; b < nbox; ++b)
-                        tma_load_2d_pair(sa + NA * kRgOperand + b * kRpBox * kRgRowBytes, &tm_b, bar, kb * kElems,
-                                         b_row + b * kRpBox, pol_x);
+                    tma_load_2d_pair(sa + NA * kRgOperand, map_b, bar, kb * kElems, b_row, pol_x);
                     issued |= 1u << stage;
                     issued_phase = (issued_phase & ~(1u << stage)) | (phase << stage);
                     if (++stage == kStages) {
@@ -910,6 +914,7 @@ struct WgradParams {
     int K, n_mt, n_nt, splits;
     uint32_t nt_inv;  // ceil(2^32 / n_nt): local / n_nt = local * nt_inv >> 32, exact for local * n_nt < 2^32
     int accumulate;  // FP32 output: add to it, groups without rows are left alone
+    int dy_blocks, x_blocks;  // the operand's map has 64-column blocks: 128 columns in one load
 };
 
 // Every role decodes every item, and a short group's item is over in ~2000 cycles: no search from the start and
@@ -1131,7 +1136,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kRwThreads, 1)
 #pragma unroll
                 for (int j = 0; j < NB; ++j) {
                     const int cols = wgrad_cols(it.k0 + 256 * j, p.K);
-                    nbox[j] = cols / 128;
+                    nbox[j] = p.x_blocks && cols ? 2 : cols / 128;  // (blocks: also those a half tile does not use)
                     b_col[j] = it.k0 + 256 * j + static_cast<int>(rank) * (cols / 2);
                     boxes += nbox[j];
                 }
@@ -1151,13 +1156,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kRwThreads, 1)
                         mbar_arrive_expect_tx(&full[stage], 2u * bytes);
                         mbar_arrive(&full[stage]);
                     }
-                    tma_load_2d_pair(sa, &tm_dy, bar, a_col, row, pol);
-                    tma_load_2d_pair(sa + kRgOperand / 2, &tm_dy, bar, a_col + 64, row, pol);
+                    if (p.dy_blocks) {
+                        tma_load_3d_pair(sa, &tm_dy, bar, 0, row, a_col / 64, pol);
+                    } else {
+                        tma_load_2d_pair(sa, &tm_dy, bar, a_col, row, pol);
+                        tma_load_2d_pair(sa + kRgOperand / 2, &tm_dy, bar, a_col + 64, row, pol);
+                    }
 #pragma unroll
-                    for (int j = 0; j < NB; ++j)
-                        for (int b = 0; b < nbox[j]; ++b)
-                            tma_load_2d_pair(sa + (1 + j) * kRgOperand + b * (kRgOperand / 2), &tm_x, bar,
-                                             b_col[j] + 64 * b, row, pol);
+                    for (int j = 0; j < NB; ++j) {
+                        uint8_t *sb = sa + (1 + j) * kRgOperand;
+                        if (p.x_blocks) {
+                            if (nbox[j]) tma_load_3d_pair(sb, &tm_x, bar, 0, row, b_col[j] / 64, pol);
+                        } else {
+                            for (int b = 0; b < nbox[j]; ++b)
+                                tma_load_2d_pair(sb + b * (kRgOperand / 2), &tm_x, bar, b_col[j] + 64 * b, row, pol);
+                        }
+                    }
                     issued |= 1u << stage;
                     issued_phase = (issued_phase & ~(1u << stage)) | (phase << stage);
                     if (++stage == kStages) {

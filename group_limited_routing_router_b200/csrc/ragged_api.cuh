@@ -105,6 +105,18 @@ bool map_groups(CUtensorMap *m, CUtensorMapDataType dt, int esize, const void *b
                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// The same rows as blocks of 64 16-bit columns [width / 64][rows][64] (width a multiple of 64), box 64 x 64 x 2:
+// 128 columns of 64 rows in one load.
+bool map_blocks(CUtensorMap *m, const void *base, uint64_t width, uint64_t ld, uint64_t rows) {
+    const cuuint64_t dims[3] = {64, rows, width / 64};
+    const cuuint64_t strides[2] = {ld * 2, 128};
+    const cuuint32_t box[3] = {64, 64, 2};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    return encode_fn()(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, box, estr,
+                       CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                       CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 constexpr int64_t kMaxLd = int64_t(1) << 32;
 int type_size(int t) { return t == BEAM_MOE_F32 ? 4 : 2; }
 bool is16(int t) { return t == BEAM_MOE_BF16 || t == BEAM_MOE_F16; }
@@ -165,7 +177,7 @@ int launch_split_any(bool i8, bool a_mn, int S, int clusters, cudaStream_t s, co
 }
 
 template <int NA>
-int launch_pair(bool i8, bool a_mn, int pairs, cudaStream_t s, const CUtensorMap &w, const CUtensorMap &b,
+int launch_pair(bool i8, bool a_mn, int pairs, cudaStream_t s, const CUtensorMap &w, const RowMaps &b,
                 const RaggedParams &p) {
     constexpr int n = RpairCfg<NA>::kSmem;
     const unsigned grid = static_cast<unsigned>(2 * pairs);
@@ -192,13 +204,16 @@ RaggedPlan ragged_plan(const RaggedDevice &d, int E, int64_t R, int M, int n_kb,
     P.few = mean <= 32;
     if (!P.few && pair_items >= d.pairs) {
         P.pair = 1;
-        // two feature tiles per pair where the rounds come out shorter: a k-step costs ~690 cycles with one,
-        // ~1060 with two, whose epilogue adds ~2000 per item (256 groups of 30 to 500 rows, 5120 x 2560:
-        // 1.25 against 1.36 ms; 64 groups of 80 to 900: 0.47 against 0.56)
+        // Two feature tiles per pair where the rounds come out shorter.  Cycles per k-step, one and two tiles: 690
+        // and 1060 where groups span several row tiles (bound by what L2 delivers), 760 and 1400 where the
+        // weights all come from HBM; two tiles add an epilogue that the products wait for.  Measured, one
+        // against two: 8 groups of 8192 rows 1.61 / 1.25 ms, 64 of 80 to 900 rows 0.60 / 0.52, 256 of 30 to
+        // 500 rows 1.38 / 1.27, 64 of 128 rows in INT8 172 / 181 us (fp32 results 172 / 188).
         if (wide_ok) {
+            const bool one_tile = mean <= 192;
             const int64_t wide_items = row_tiles * ((M + 2 * kPairRows - 1) / (2 * kPairRows));
-            const int64_t t1 = (pair_items + d.pairs - 1) / d.pairs * n_kb * 690;
-            const int64_t t2 = (wide_items + d.pairs - 1) / d.pairs * (n_kb * int64_t(1060) + 2000);
+            const int64_t t1 = (pair_items + d.pairs - 1) / d.pairs * n_kb * (one_tile ? 760 : 690);
+            const int64_t t2 = (wide_items + d.pairs - 1) / d.pairs * (n_kb * int64_t(one_tile ? 1400 : 1060) + 2500);
             if (t2 < t1) P.pair = 2;
         }
         return P;
@@ -274,16 +289,24 @@ int ragged_product(const RaggedCall &c, cudaStream_t s) {
     p.row_scale = c.row_scale;
     p.channel_scale = c.channel_scale;
     p.timeout = kDefaultTimeoutCycles;
-    const int box = P.pair ? kRpBox : (P.few ? RsplitCfg<RS_FEW_ARGS>::kBox : RsplitCfg<RS_MID_ARGS>::kBox);
-    CUtensorMap m_w, m_b;
+    const uint32_t kbox = static_cast<uint32_t>(kelems);
+    CUtensorMap m_w;
     // dgrad's weight tile is 64 features (K, contiguous) by 64 contraction rows (N), two boxes per 128 features
     if (!map_groups(&m_w, esize == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, esize, c.w,
-                    c.K, c.N, c.E, static_cast<uint32_t>(kelems), c.dgrad ? 64 : kBM) ||
-        !map_rows(&m_b, esize, c.rows, width, c.ld_rows, c.R, static_cast<uint32_t>(kelems), static_cast<uint32_t>(box)))
+                    c.K, c.N, c.E, kbox, c.dgrad ? 64 : kBM))
         return BEAM_MOE_ERR_CUDA;
-    if (P.pair)
+    if (P.pair) {
+        RowMaps m_b;
+        for (int i = 0; i < kRpBoxes; ++i)
+            if (!map_rows(&m_b.m[i], esize, c.rows, width, c.ld_rows, c.R, kbox, static_cast<uint32_t>((i + 1) * kRpBoxStep)))
+                return BEAM_MOE_ERR_CUDA;
         return P.pair == 1 ? launch_pair<1>(c.i8, c.dgrad, d.pairs, s, m_w, m_b, p)
                            : launch_pair<2>(c.i8, c.dgrad, d.pairs, s, m_w, m_b, p);
+    }
+    CUtensorMap m_b;
+    if (!map_rows(&m_b, esize, c.rows, width, c.ld_rows, c.R, kbox,
+                  P.few ? RsplitCfg<RS_FEW_ARGS>::kBox : RsplitCfg<RS_MID_ARGS>::kBox))
+        return BEAM_MOE_ERR_CUDA;
     // items is an estimate where there are offsets: keep the whole GPU for uneven groups
     const int clusters = c.offsets ? d.clusters[P.log_s] : std::min(P.items, d.clusters[P.log_s]);
     return P.few ? launch_split_any<RS_FEW_ARGS>(c.i8, c.dgrad, P.S, clusters, s, m_w, m_b, p)
@@ -333,11 +356,12 @@ int launch_swiglu(int dtype, const SwigluParams &p, cudaStream_t s) {
 
 template <typename T, bool SWIGLU>
 int launch_quant_t(const QuantParams &p, cudaStream_t s) {
+    constexpr int kSteps = kQuantCached;
     const int vecs = p.K / 8;
-    if (vecs <= 32 * kQuantCached) {
+    if (vecs <= 32 * kSteps) {
         quant_i8_kernel<T, SWIGLU, true><<<static_cast<unsigned>((p.R + 7) / 8), 256, 0, s>>>(p);
     } else {
-        const int threads = std::min(512, ((vecs + 1) / 2 + 31) / 32 * 32);
+        const int threads = std::min(512, ((vecs + kSteps - 1) / kSteps + 31) / 32 * 32);
         quant_i8_kernel<T, SWIGLU, false><<<static_cast<unsigned>(p.R), threads, 0, s>>>(p);
     }
     return launch_status();
@@ -443,7 +467,10 @@ int beam_moe_grouped_mm_wgrad(int32_t n_experts, int64_t R, int32_t K, int32_t N
                                                          : (store == BEAM_MOE_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
                                                                                   : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16);
     CUtensorMap m_dy, m_x, m_dw;
-    if (!map_rows(&m_dy, 2, dy, N, ldy, R, 64, 64) || !map_rows(&m_x, 2, x, K, ldx, R, 64, 64) ||
+    p.dy_blocks = N % 64 == 0;
+    p.x_blocks = K % 64 == 0;
+    if (!(p.dy_blocks ? map_blocks(&m_dy, dy, N, ldy, R) : map_rows(&m_dy, 2, dy, N, ldy, R, 64, 64)) ||
+        !(p.x_blocks ? map_blocks(&m_x, x, K, ldx, R) : map_rows(&m_x, 2, x, K, ldx, R, 64, 64)) ||
         !map_groups(&m_dw, dt, type_size(store), splits > 1 ? ws : dw, K, N, static_cast<uint64_t>(splits) * n_experts,
                     128u / static_cast<uint32_t>(type_size(store)), 32))
         return BEAM_MOE_ERR_CUDA;

@@ -13,34 +13,43 @@
 
 namespace beam {
 
-// Plain loads: the outputs of a call may be its inputs' buffers.
+// Eight elements as loaded, and as FP32.  Plain loads: the outputs of a call may be its inputs' buffers.
 template <typename T>
-__device__ __forceinline__ void load8(const T *p, float (&v)[8]);
-template <>
-__device__ __forceinline__ void load8(const float *p, float (&v)[8]) {
-    const float4 a = reinterpret_cast<const float4 *>(p)[0], b = reinterpret_cast<const float4 *>(p)[1];
-    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+struct Raw8 {
+    uint4 w[sizeof(T) / 2];
+};
+template <typename T>
+__device__ __forceinline__ Raw8<T> load_raw(const T *p) {
+    Raw8<T> r;
+#pragma unroll
+    for (int i = 0; i < static_cast<int>(sizeof(T) / 2); ++i) r.w[i] = reinterpret_cast<const uint4 *>(p)[i];
+    return r;
 }
-template <>
-__device__ __forceinline__ void load8(const __nv_bfloat16 *p, float (&v)[8]) {
-    const uint4 a = *reinterpret_cast<const uint4 *>(p);
-    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+__device__ __forceinline__ void unpack(const Raw8<float> &r, float (&v)[8]) {
+    const uint32_t w[8] = {r.w[0].x, r.w[0].y, r.w[0].z, r.w[0].w, r.w[1].x, r.w[1].y, r.w[1].z, r.w[1].w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(w[i]);
+}
+__device__ __forceinline__ void unpack(const Raw8<__nv_bfloat16> &r, float (&v)[8]) {
+    const uint32_t w[4] = {r.w[0].x, r.w[0].y, r.w[0].z, r.w[0].w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         v[2 * i] = __uint_as_float(w[i] << 16);
         v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
     }
 }
-template <>
-__device__ __forceinline__ void load8(const __half *p, float (&v)[8]) {
-    const uint4 a = *reinterpret_cast<const uint4 *>(p);
-    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+__device__ __forceinline__ void unpack(const Raw8<__half> &r, float (&v)[8]) {
+    const uint32_t w[4] = {r.w[0].x, r.w[0].y, r.w[0].z, r.w[0].w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w[i]));
         v[2 * i] = f.x;
         v[2 * i + 1] = f.y;
     }
+}
+template <typename T>
+__device__ __forceinline__ void load8(const T *p, float (&v)[8]) {
+    unpack(load_raw(p), v);
 }
 __device__ __forceinline__ void store8(float *p, const float (&v)[8]) {
     reinterpret_cast<float4 *>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
@@ -65,12 +74,28 @@ __device__ __forceinline__ void store8(__half *p, const float (&v)[8]) {
     *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// sigma(g): for 16-bit data with the fast exponential and division (a few FP32 ulp, far below the result's
-// rounding), for fp32 with the accurate ones.  g -> -inf: exp overflows to +inf and the quotient is 0.
+// 2^x to within a few 2^-23 (the hardware's approximation; overflows to +inf, underflows to 0).
+__device__ __forceinline__ float exp2_fast(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+// sigma(g) = 1 / (1 + e^-g).  16-bit data: the fast exponential and quotient, whose error (|g| 2^-24 from the
+// rounded product with log2 e) is far below the result's rounding.  fp32 data: that product's rounding error is
+// kept and applied to first order, e^x = 2^p (1 + r ln 2) with p + r = x log2 e, which leaves a few 2^-23; the
+// argument is clamped where e^x is 0 or +inf anyway, so that r stays small.
 template <typename T>
 __device__ __forceinline__ float sigmoid_of(float g) {
-    if constexpr (sizeof(T) == 2) return __fdividef(1.0f, 1.0f + __expf(-g));
-    else return __fdiv_rn(1.0f, 1.0f + expf(-g));
+    if constexpr (sizeof(T) == 2) {
+        return __fdividef(1.0f, 1.0f + __expf(-g));
+    } else {
+        constexpr float kLog2e = 1.44269504f, kLog2eLow = 1.92596299e-8f, kLn2 = 0.693147181f;
+        const float x = g != g ? g : fminf(fmaxf(-g, -126.0f), 126.0f);
+        const float p = x * kLog2e;
+        const float r = fmaf(x, kLog2eLow, fmaf(x, kLog2e, -p));
+        const float e = exp2_fast(p);
+        return __fdividef(1.0f, 1.0f + fmaf(e, r * kLn2, e));
+    }
 }
 
 struct SwigluParams {
@@ -126,54 +151,95 @@ struct QuantParams {
     int K;
 };
 
+// Eight values of a row as loaded (SWIGLU: of both operands), and what is quantised of them.
 template <typename T, bool SWIGLU>
-__device__ __forceinline__ void quant_values(const QuantParams &p, int64_t r, int c, float (&v)[8]) {
-    load8(reinterpret_cast<const T *>(p.x) + r * p.ld_x + c, v);
-    if constexpr (SWIGLU) {
-        float u[8];
-        load8(reinterpret_cast<const T *>(p.u) + r * p.ld_u + c, u);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = v[i] * sigmoid_of<T>(v[i]) * u[i];
+struct QuantRaw {
+    Raw8<T> x[SWIGLU ? 2 : 1];
+    __device__ __forceinline__ void load(const QuantParams &p, int64_t r, int c) {
+        x[0] = load_raw(reinterpret_cast<const T *>(p.x) + r * p.ld_x + c);
+        if constexpr (SWIGLU) x[1] = load_raw(reinterpret_cast<const T *>(p.u) + r * p.ld_u + c);
     }
-}
-__device__ __forceinline__ void quant_store(int8_t *q, const float (&v)[8], float s) {
+    __device__ __forceinline__ void values(float (&v)[8]) const {
+        unpack(x[0], v);
+        if constexpr (SWIGLU) {
+            float u[8];
+            unpack(x[1], u);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = v[i] * sigmoid_of<T>(v[i]) * u[i];
+        }
+    }
+};
+// Codes of eight values: the integers nearest to v / s (the FP32 quotient).  With inv = 1 / s the product v * inv
+// is within 1.5 units of the last place of the quotient (2.3e-5 at 127), so its nearest integer is the same one
+// unless it lies next to a half; only then are the quotients formed (the division of every element would
+// take longer than the memory traffic).  Adding 1.5 x 2^23 rounds to an integer, ties to even, and leaves its
+// two's complement in the low bits.
+__device__ __forceinline__ void quant_store(int8_t *q, const float (&v)[8], float s, float inv) {
     uint32_t w[2] = {0u, 0u};
     if (s > 0.0f && s < INFINITY) {
+        constexpr float kMagic = 12582912.0f;
+        float y[8];
+        bool clear = true;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            // a scale among the subnormals can round the quotient past 127
-            const int c = max(-127, min(127, __float2int_rn(__fdiv_rn(v[i], s))));
-            w[i >> 2] |= (static_cast<uint32_t>(c) & 0xFFu) << (8 * (i & 3));
+            const float t = v[i] * inv;
+            y[i] = t + kMagic;
+            clear = clear && fabsf(t - (y[i] - kMagic)) <= 0.4999f;  // false for NaN and infinities (s subnormal)
+        }
+        if (!clear) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)  // a subnormal s can round the quotient past 127
+                y[i] = fminf(fmaxf(__fdiv_rn(v[i], s), -127.0f), 127.0f) + kMagic;
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const uint32_t lo = __byte_perm(__float_as_uint(y[4 * i]), __float_as_uint(y[4 * i + 1]), 0x0040);
+            const uint32_t hi = __byte_perm(__float_as_uint(y[4 * i + 2]), __float_as_uint(y[4 * i + 3]), 0x0040);
+            w[i] = __byte_perm(lo, hi, 0x5410);
         }
     }
     *reinterpret_cast<uint2 *>(q) = make_uint2(w[0], w[1]);
 }
 
-constexpr int kQuantCached = 4;  // steps whose values stay in registers between the two passes
+// Steps of eight elements that a thread keeps in registers between the two passes (x as loaded, or SwiGLU's
+// FP32 values).
+constexpr int kQuantCached = 4;
 
 // One row per warp (WARP_ROW: short rows, 8 rows per CTA) or per CTA: the largest magnitude of the row,
-// then its codes.  Values past the cached steps (K > 16384) are read again.
+// then its codes.  All of a thread's loads are issued before the first is used, and CTAs are kept small, so that
+// enough rows are in flight per SM (8192 x 5120 bf16: 36 us; with 96 threads of
+// seven steps 38 to 45 us, with 320 of two 44, with a warp of twenty 71).
+// Values past the cached steps are read again.
 template <typename T, bool SWIGLU, bool WARP_ROW>
 __global__ void __launch_bounds__(512) quant_i8_kernel(const QuantParams p) {
+    constexpr int kSteps = kQuantCached;
     __shared__ float part[16];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t r = WARP_ROW ? static_cast<int64_t>(blockIdx.x) * (blockDim.x >> 5) + warp : blockIdx.x;
     if (WARP_ROW && r >= p.R) return;
     const int me = WARP_ROW ? lane : threadIdx.x, all = WARP_ROW ? 32 : blockDim.x;
-    float v[kQuantCached][8];
+    QuantRaw<T, SWIGLU> raw[kSteps];
+    float h[SWIGLU ? kSteps : 1][8];
     float m = 0.0f;
 #pragma unroll
-    for (int i = 0; i < kQuantCached; ++i) {
-        const int c = (me + i * all) * 8;
-        if (c < p.K) {
-            quant_values<T, SWIGLU>(p, r, c, v[i]);
+    for (int i = 0; i < kSteps; ++i)
+        if ((me + i * all) * 8 < p.K) raw[i].load(p, r, (me + i * all) * 8);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) m = max_nan(m, fabsf(v[i][j]));
+    for (int i = 0; i < kSteps; ++i)
+        if ((me + i * all) * 8 < p.K) {
+            float t[8];
+            raw[i].values(t);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                m = max_nan(m, fabsf(t[j]));
+                if constexpr (SWIGLU) h[i][j] = t[j];
+            }
         }
-    }
-    for (int c = (me + kQuantCached * all) * 8; c < p.K; c += all * 8) {
+    for (int c = (me + kSteps * all) * 8; c < p.K; c += all * 8) {
+        QuantRaw<T, SWIGLU> more;
         float t[8];
-        quant_values<T, SWIGLU>(p, r, c, t);
+        more.load(p, r, c);
+        more.values(t);
 #pragma unroll
         for (int j = 0; j < 8; ++j) m = max_nan(m, fabsf(t[j]));
     }
@@ -185,18 +251,28 @@ __global__ void __launch_bounds__(512) quant_i8_kernel(const QuantParams p) {
         m = part[0];
         for (int w = 1; w < static_cast<int>(blockDim.x >> 5); ++w) m = max_nan(m, part[w]);
     }
-    const float s = __fdiv_rn(m, 127.0f);
+    const float s = __fdiv_rn(m, 127.0f), inv = __fdiv_rn(1.0f, s);
     if (me == 0) p.scale[r] = s;
     int8_t *q = p.q + r * static_cast<int64_t>(p.K);
 #pragma unroll
-    for (int i = 0; i < kQuantCached; ++i) {
+    for (int i = 0; i < kSteps; ++i) {
         const int c = (me + i * all) * 8;
-        if (c < p.K) quant_store(q + c, v[i], s);
+        if (c < p.K) {
+            if constexpr (SWIGLU) {
+                quant_store(q + c, h[i], s, inv);
+            } else {
+                float t[8];
+                raw[i].values(t);
+                quant_store(q + c, t, s, inv);
+            }
+        }
     }
-    for (int c = (me + kQuantCached * all) * 8; c < p.K; c += all * 8) {
+    for (int c = (me + kSteps * all) * 8; c < p.K; c += all * 8) {
+        QuantRaw<T, SWIGLU> more;
         float t[8];
-        quant_values<T, SWIGLU>(p, r, c, t);
-        quant_store(q + c, t, s);
+        more.load(p, r, c);
+        more.values(t);
+        quant_store(q + c, t, s, inv);
     }
 }
 
