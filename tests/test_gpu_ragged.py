@@ -226,6 +226,29 @@ def test_weight_gradient_accumulates(E, R, N, K):
         assert torch.equal(dw[3], before[3])
 
 
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("counts", [[0, 5107, 300], [5107], [64, 0, 0, 6001]])
+def test_weight_gradient_of_long_groups(counts, dtype):
+    """The 512-column tiles: groups of more rows than one flush of fp32 results (4096) beside empty ones."""
+    E, R, N, K = len(counts), sum(counts), 1016, 2568
+    g = gen(R)
+    dy, x = normal(g, R, N, dtype=dtype), normal(g, R, K, dtype=dtype)
+    off = offsets_of(counts)
+    v, mag = products(x, dy, torch.zeros(E, N, K, device="cuda"), counts)["dw"]
+    for out_dtype in (dtype, F32):
+        check(bm.grouped_mm_wgrad(dy, x, off, out_dtype=out_dtype), v,
+              half_step(v, out_dtype) + sum_tol(mag, max(counts), out_dtype), f"{out_dtype}")
+    before = torch.randn(E, N, K, generator=g, device="cuda")
+    dw = before.clone()
+    bm.grouped_mm_wgrad(dy, x, off, out=dw, accumulate=True)
+    want = before.to(D) + v
+    check(dw, want, half_step(want, F32) + sum_tol(mag + before.abs(), max(counts), F32), "accumulated")
+    for e, c in enumerate(counts):
+        if c == 0:
+            assert torch.equal(dw[e], before[e])
+    status_ok()
+
+
 def test_gradients_against_differences():
     """out is linear in x and in w: the change of sum(dy * out) along any direction is its gradient times
     that direction, exactly but for the roundings (fp32 results)."""
