@@ -634,7 +634,8 @@ def dense_swiglu(x, w_gate, w_up, w_down, y=None, ws=None, stream=None):
 
 # ---- the experts' steps as operators of their own, with their gradients ---------------------------
 # Matrices over rows may be strided (unit column stride, rows on 16-byte boundaries), every other tensor is
-# contiguous.  A call runs on its tensors' device, on `stream` (default: that device's current stream).
+# contiguous.  A call runs on its tensors' device, on `stream` (default: that device's current stream), and
+# allocates what it returns on that stream.  Gradients are calls of their own: nothing here records autograd.
 TYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 _HALF = (torch.bfloat16, torch.float16)
 
@@ -646,7 +647,9 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
 
 def _rows(t, name: str, dtypes, device=None, shape=None) -> int:
     """Checks a [rows, width] operand; its row stride."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+    if not isinstance(t, torch.Tensor) or not (t.is_cuda if device is None else t.device == device):
+        if isinstance(t, torch.Tensor) and t.is_cuda:
+            raise ValueError(f"{name} is on {t.device}, expected {device}")
         raise TypeError(f"{name} must be a CUDA tensor (there is no CPU path)")
     if t.dtype not in dtypes:
         raise TypeError(f"{name} must be one of {[str(d) for d in dtypes]}, got {t.dtype}")
@@ -661,37 +664,45 @@ def _rows(t, name: str, dtypes, device=None, shape=None) -> int:
         ld = width
     elif ld < width:
         raise ValueError(f"{name} has overlapping rows (row stride {ld} < {width})")
-    if device is not None and t.device != device:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
     if shape is not None and size != shape:
         raise ValueError(f"{name} has shape {tuple(size)}, expected {tuple(shape)}")
     return ld
 
 
 def _on(t, name: str, dtype, shape, device):
-    """_dev, on `device`."""
+    """_dev of a tensor that has to be there, on `device`."""
+    if t is None:
+        raise TypeError(f"{name} must be a CUDA tensor, got None")
     _dev(t, name, dtype, shape)
     if t.device != device:
         raise ValueError(f"{name} is on {t.device}, expected {device}")
     return t
 
 
-def _out_rows(out, name: str, dtype, R: int, width: int, device):
+def _empty(shape, dtype, device, stream) -> torch.Tensor:
+    """A tensor for the call's stream: memory that other work of that stream has left, not of the current one."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream),
+                                           device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _out_rows(out, name: str, dtype, R: int, width: int, device, stream):
     """(out, its row stride), allocated where `out` is None."""
     if out is None:
-        return torch.empty((R, width), dtype=dtype, device=device), width
+        return _empty((R, width), dtype, device, stream), width
     return out, _rows(out, name, (dtype,), device, (R, width))
 
 
-def _run(where: str, device, stream, *args, scratch=None):
+def _run(where: str, device, stream, *args):
     """Calls entry point `where` with `args` and the stream, on `device`."""
     if stream is None:
         handle = _raw_stream(device.index)
     else:
         handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
-        if scratch is not None:  # allocated here, used there: its memory stays taken until that stream is done
-            scratch.record_stream(stream if isinstance(stream, torch.cuda.Stream)
-                                  else torch.cuda.ExternalStream(handle, device=device))
     fn = getattr(_lib or lib(), where)
     if torch.cuda.current_device() == device.index:
         code = fn(*args, handle)
@@ -743,7 +754,7 @@ def grouped_mm(x, w, offsets=None, out=None, out_dtype=None, stream=None) -> tor
     if K != Kw:
         raise ValueError(f"x has {K} columns, w expects {Kw}")
     od = _out_type(out, out_dtype, dtype)
-    out, ldo = _out_rows(out, "out", od, R, N, device)
+    out, ldo = _out_rows(out, "out", od, R, N, device, stream)
     _run("beam_moe_grouped_mm", device, stream, E, R, K, N, TYPES[dtype], x.data_ptr(), ldx,
          _groups_of(offsets, E, device), w.data_ptr(), TYPES[od], out.data_ptr(), ldo)
     return out
@@ -758,7 +769,7 @@ def grouped_mm_dgrad(dy, w, offsets=None, out=None, out_dtype=None, stream=None)
     if N != Nw:
         raise ValueError(f"dy has {N} columns, w expects {Nw}")
     od = _out_type(out, out_dtype, dtype)
-    out, ldx = _out_rows(out, "out", od, R, K, device)
+    out, ldx = _out_rows(out, "out", od, R, K, device, stream)
     _run("beam_moe_grouped_mm_dgrad", device, stream, E, R, K, N, TYPES[dtype], dy.data_ptr(), ldy,
          _groups_of(offsets, E, device), w.data_ptr(), TYPES[od], out.data_ptr(), ldx)
     return out
@@ -774,33 +785,39 @@ def grouped_mm_wgrad(dy, x, offsets=None, out=None, out_dtype=None, accumulate: 
     (R, N), K = dy.shape, x.shape[1]
     if x.shape[0] != R:
         raise ValueError(f"dy has {R} rows, x {x.shape[0]}")
-    E = 1 if offsets is None else offsets.numel() - 1
+    E = 1
+    if offsets is not None:
+        _on(offsets, "offsets", torch.int64, None, dy.device)
+        E = offsets.numel() - 1
+        if offsets.dim() != 1 or E < 1:
+            raise ValueError(f"offsets has shape {tuple(offsets.shape)}, expected [experts + 1]")
     od = _out_type(out, out_dtype, dy.dtype)
     if out is None:
         if accumulate:
             raise ValueError("accumulate needs out, the fp32 gradient to add to")
-        out = torch.empty(E, N, K, dtype=od, device=dy.device)
-    _on(out, "out", od, (E, N, K) if out.dim() == 3 or E != 1 else (N, K), dy.device)
-    need = int(lib().beam_moe_grouped_mm_wgrad_workspace_size(E, R, K, N))
-    scratch = None
-    if ws is None:
-        if need:
-            ws = scratch = torch.empty(need, dtype=torch.uint8, device=dy.device)
+        out = _empty((E, N, K), od, dy.device, stream)
     else:
+        _on(out, "out", od, None, dy.device)
+        if tuple(out.shape) != (E, N, K) and (E != 1 or tuple(out.shape) != (N, K)):
+            raise ValueError(f"out has shape {tuple(out.shape)}, expected {(E, N, K)}")
+    need = int(lib().beam_moe_grouped_mm_wgrad_workspace_size(E, R, K, N))
+    if ws is not None:
         _on(ws, "ws", torch.uint8, None, dy.device)
+    elif need:
+        ws = _empty((need,), torch.uint8, dy.device, stream)
     _run("beam_moe_grouped_mm_wgrad", dy.device, stream, E, R, K, N, TYPES[dy.dtype], dy.data_ptr(), ldy,
-         x.data_ptr(), ldx, _groups_of(offsets, E, dy.device), TYPES[od], out.data_ptr(), int(bool(accumulate)),
-         None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel(), scratch=scratch)
+         x.data_ptr(), ldx, None if offsets is None else offsets.data_ptr(), TYPES[od], out.data_ptr(),
+         int(bool(accumulate)), None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel())
     return out
 
 
-def _codes(q, scale, R: int, K: int, device):
+def _codes(q, scale, R: int, K: int, device, stream):
     if q is None:
-        q = torch.empty((R, K), dtype=torch.int8, device=device)
+        q = _empty((R, K), torch.int8, device, stream)
     else:
         _on(q, "q", torch.int8, (R, K), device)
     if scale is None:
-        scale = torch.empty(R, dtype=torch.float32, device=device)
+        scale = _empty((R,), torch.float32, device, stream)
     else:
         _on(scale, "scale", torch.float32, (R,), device)
     return q, scale
@@ -810,7 +827,7 @@ def quant_i8_rows(x, q=None, scale=None, stream=None):
     """(q [R, K] int8, scale [R] fp32): scale = max|x[r]| / 127, q = x / scale to the nearest integer."""
     ldx = _rows(x, "x", TYPES)
     R, K = x.shape
-    q, scale = _codes(q, scale, R, K, x.device)
+    q, scale = _codes(q, scale, R, K, x.device, stream)
     _run("beam_moe_quant_i8_rows", x.device, stream, R, K, TYPES[x.dtype], x.data_ptr(), ldx, q.data_ptr(),
          scale.data_ptr())
     return q, scale
@@ -835,7 +852,7 @@ def grouped_mm_i8(q, row_scale, w, channel_scale, offsets=None, out=None, out_dt
     _on(row_scale, "row_scale", torch.float32, (R,), device)
     _on(channel_scale, "channel_scale", torch.float32, (E, N), device)
     od = _out_type(out, out_dtype, torch.bfloat16)
-    out, ldo = _out_rows(out, "out", od, R, N, device)
+    out, ldo = _out_rows(out, "out", od, R, N, device, stream)
     _run("beam_moe_grouped_mm_i8", device, stream, E, R, K, N, q.data_ptr(), row_scale.data_ptr(),
          _groups_of(offsets, E, device), w.data_ptr(), channel_scale.data_ptr(), TYPES[od], out.data_ptr(), ldo)
     return out
@@ -847,7 +864,7 @@ def swiglu(g, u, out=None, stream=None) -> torch.Tensor:
     R, I = size = g.shape
     device, types = g.device, (g.dtype,)
     ldu = _rows(u, "u", types, device, size)
-    out, ldo = _out_rows(out, "out", g.dtype, R, I, device)
+    out, ldo = _out_rows(out, "out", g.dtype, R, I, device, stream)
     _run("beam_moe_swiglu", device, stream, R, I, TYPES[g.dtype], g.data_ptr(), ldg, u.data_ptr(), ldu,
          out.data_ptr(), ldo)
     return out
@@ -860,8 +877,8 @@ def swiglu_backward(dh, g, u, dg=None, du=None, stream=None):
     device, types = g.device, (g.dtype,)
     ldu = _rows(u, "u", types, device, size)
     lddh = _rows(dh, "dh", types, device, size)
-    dg, lddg = _out_rows(dg, "dg", g.dtype, R, I, device)
-    du, lddu = _out_rows(du, "du", g.dtype, R, I, device)
+    dg, lddg = _out_rows(dg, "dg", g.dtype, R, I, device, stream)
+    du, lddu = _out_rows(du, "du", g.dtype, R, I, device, stream)
     _run("beam_moe_swiglu_backward", device, stream, R, I, TYPES[g.dtype], dh.data_ptr(), lddh, g.data_ptr(),
          ldg, u.data_ptr(), ldu, dg.data_ptr(), lddg, du.data_ptr(), lddu)
     return dg, du
@@ -873,7 +890,7 @@ def swiglu_i8(g, u, q=None, scale=None, stream=None):
     R, I = size = g.shape
     device, types = g.device, (g.dtype,)
     ldu = _rows(u, "u", types, device, size)
-    q, scale = _codes(q, scale, R, I, device)
+    q, scale = _codes(q, scale, R, I, device, stream)
     _run("beam_moe_swiglu_i8", device, stream, R, I, TYPES[g.dtype], g.data_ptr(), ldg, u.data_ptr(), ldu,
          q.data_ptr(), scale.data_ptr())
     return q, scale

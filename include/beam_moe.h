@@ -23,7 +23,8 @@
  *     the kernels (a bad expert id, a wait that timed out) are recorded in a per-device status
  *     word that beam_moe_device_status returns.
  *   - x, y, weights and the workspace must be 16-byte aligned; hidden and inter must be
- *     multiples of 64.  T = 0 is valid and does nothing.
+ *     multiples of 64.  T = 0 is valid and does nothing.  (The operators on rows at the end of this
+ *     file take strided rows and other widths; they say so.)
  *   - Readings where the pages are silent: groups are contiguous index ranges; ties go to the
  *     lower group / expert index; slot j of a token holds its j-th best expert (descending
  *     selection value); an optional per-expert selection bias is added to the scores for group
@@ -70,8 +71,8 @@ enum {
     BEAM_MOE_ERR_UNSUPPORTED_DEVICE = 5, /* the current device is not compute capability 10.0 */
     BEAM_MOE_ERR_CUDA = 6,               /* a CUDA runtime / launch error */
     BEAM_MOE_ERR_DEVICE_TIMEOUT = 7,     /* status word: a bounded device-side wait expired */
-    BEAM_MOE_ERR_BAD_INDEX = 8,          /* status word: an expert id outside [0, E) */
-    BEAM_MOE_ERR_INVALID_ARG = 9         /* T < 0, T > 2^24 or T * k >= 2^31 */
+    BEAM_MOE_ERR_BAD_INDEX = 8,          /* status word: an expert id outside [0, E), or bad group offsets */
+    BEAM_MOE_ERR_INVALID_ARG = 9         /* T < 0, T > 2^24 or T * k >= 2^31; a type or row stride out of range */
 };
 
 /* Workspace kinds for beam_moe_workspace_size. */

@@ -593,11 +593,18 @@ def test_binding_refusals():
               lambda: bm.grouped_mm(x, w.transpose(0, 1), off),              # weights not packed
               lambda: bm.grouped_mm(x, w, off, out=torch.empty(5, 32, dtype=BF, device="cuda")),
               lambda: bm.grouped_mm_wgrad(x, x[:5], off),
+              lambda: bm.grouped_mm_wgrad(x, x, off[:1]),
+              lambda: bm.grouped_mm_wgrad(x, x, off, out=torch.empty(2, 64, 32, dtype=BF, device="cuda")),
               lambda: bm.grouped_mm_wgrad(x, x, off, accumulate=True),
               lambda: bm.swiglu(x, x[:5])):
         with pytest.raises(ValueError):
             f()
-    for f in (lambda: bm.grouped_mm(x, w.to(HF), off), lambda: bm.grouped_mm(x.float(), w.float(), off),
+    one = torch.ones(2, 32, device="cuda")
+    q, s = bm.quant_i8_rows(x)
+    for f in (lambda: bm.grouped_mm_i8(q, None, w.to(torch.int8), one, off),
+              lambda: bm.grouped_mm_i8(q, s, w.to(torch.int8), None, off), lambda: bm.grouped_mm(x, None, off),
+              lambda: bm.grouped_mm_wgrad(x, x, [0, 2, 6]), lambda: bm.swiglu(x, None),
+              lambda: bm.grouped_mm(x, w.to(HF), off), lambda: bm.grouped_mm(x.float(), w.float(), off),
               lambda: bm.grouped_mm(x, w, off.int()), lambda: bm.grouped_mm(x, w, off, out_dtype=torch.int8),
               lambda: bm.grouped_mm(x, w, off, out=torch.empty(6, 32, device="cuda"), out_dtype=BF),
               lambda: bm.swiglu(x, x.float())):
@@ -621,6 +628,11 @@ def test_on_another_stream():
     side.wait_stream(torch.cuda.current_stream())
     got = dict(out=bm.grouped_mm(x, w, stream=side), dx=bm.grouped_mm_dgrad(dy, w, stream=side),
                dw=bm.grouped_mm_wgrad(dy, x, stream=side))
+    side.synchronize()
+    assert all(torch.equal(got[k], want[k]) for k in want)
+    # by its handle; what a call returns belongs to that stream, whose later work may use it unordered
+    got = dict(out=bm.grouped_mm(x, w, stream=side.cuda_stream), dx=bm.grouped_mm_dgrad(dy, w, stream=side.cuda_stream),
+               dw=bm.grouped_mm_wgrad(dy, x, stream=side.cuda_stream))
     side.synchronize()
     assert all(torch.equal(got[k], want[k]) for k in want)
     status_ok()
