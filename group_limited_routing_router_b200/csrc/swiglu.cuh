@@ -136,10 +136,36 @@ __global__ void __launch_bounds__(256) swiglu_kernel(const SwigluParams p) {
     }
 }
 
-__device__ __forceinline__ float max_nan(float a, float b) {  // NaN if either is
-    float r;
-    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
-    return r;
+// Largest magnitude of eight values as an unsigned pattern: magnitudes compare like their bits, with infinity above
+// every number and NaN above infinity.  16-bit data stay packed, two to an instruction; `magnitude` turns the
+// pattern (for packed ones, of the two halves) into a float.
+template <typename T>
+__device__ __forceinline__ uint32_t most_bits(uint32_t m, const Raw8<T> &r) {
+#pragma unroll
+    for (int i = 0; i < static_cast<int>(sizeof(T) / 2); ++i) {
+        const uint32_t w[4] = {r.w[i].x, r.w[i].y, r.w[i].z, r.w[i].w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            m = sizeof(T) == 4 ? max(m, w[j] & 0x7FFFFFFFu) : __vmaxu2(m, w[j] & 0x7FFF7FFFu);
+    }
+    return m;
+}
+template <typename T>
+__device__ __forceinline__ float magnitude(uint32_t m) {
+    if constexpr (sizeof(T) == 4) {
+        return __uint_as_float(m);
+    } else {
+        Raw8<T> r{};
+        r.w[0].x = max(m & 0xFFFFu, m >> 16);
+        float v[8];
+        unpack(r, v);
+        return v[0];
+    }
+}
+__device__ __forceinline__ uint32_t most_of(uint32_t m, const float (&v)[8]) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) m = max(m, __float_as_uint(v[j]) & 0x7FFFFFFFu);
+    return m;
 }
 
 struct QuantParams {
@@ -169,24 +195,27 @@ struct QuantRaw {
         }
     }
 };
-// Codes of eight values: the integers nearest to v / s (the FP32 quotient).  With inv = 1 / s the product v * inv
-// is within 1.5 units of the last place of the quotient (2.3e-5 at 127), so its nearest integer is the same one
-// unless it lies next to a half; only then are the quotients formed (the division of every element would
-// take longer than the memory traffic).  Adding 1.5 x 2^23 rounds to an integer, ties to even, and leaves its
-// two's complement in the low bits.
+// Codes of eight values: the integers nearest to the FP32 quotients v / s, with inv = 1 / s to nearest.  The
+// quotient comes from v * inv by two of Markstein's corrections (P. W. Markstein, "Computation of elementary
+// functions on the IBM RISC System/6000 processor", 1990): the first leaves it within a unit of its last
+// place, and from there the second gives the quotient to nearest, as long as the residuals v - q s are exact,
+// which they are for s >= 2^-100.  No element needs a branch (a bf16 row often holds half of its own largest
+// magnitude, whose quotient 63.5 is a tie, so a test for nearby halves sent a quarter of all warps through the
+// divisions).  Adding 1.5 x 2^23 rounds to an integer, ties to even, and leaves its two's complement in the low bits.
 __device__ __forceinline__ void quant_store(int8_t *q, const float (&v)[8], float s, float inv) {
     uint32_t w[2] = {0u, 0u};
     if (s > 0.0f && s < INFINITY) {
         constexpr float kMagic = 12582912.0f;
         float y[8];
-        bool clear = true;
+        if (s >= 0x1p-100f) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float t = v[i] * inv;
-            y[i] = t + kMagic;
-            clear = clear && fabsf(t - (y[i] - kMagic)) <= 0.4999f;  // false for NaN and infinities (s subnormal)
-        }
-        if (!clear) {
+            for (int i = 0; i < 8; ++i) {
+                float t = v[i] * inv;
+                t = fmaf(fmaf(-t, s, v[i]), inv, t);
+                t = fmaf(fmaf(-t, s, v[i]), inv, t);
+                y[i] = t + kMagic;
+            }
+        } else {
 #pragma unroll
             for (int i = 0; i < 8; ++i)  // a subnormal s can round the quotient past 127
                 y[i] = fminf(fmaxf(__fdiv_rn(v[i], s), -127.0f), 127.0f) + kMagic;
@@ -207,51 +236,53 @@ constexpr int kQuantCached = 4;
 
 // One row per warp (WARP_ROW: short rows, 8 rows per CTA) or per CTA: the largest magnitude of the row,
 // then its codes.  All of a thread's loads are issued before the first is used, and CTAs are kept small, so that
-// enough rows are in flight per SM (8192 x 5120 bf16: 36 us; with 96 threads of
+// enough rows are in flight per SM (8192 x 5120 bf16: 30 us; before the quotients lost their branches 36, with 96 threads of
 // seven steps 38 to 45 us, with 320 of two 44, with a warp of twenty 71).
 // Values past the cached steps are read again.
 template <typename T, bool SWIGLU, bool WARP_ROW>
 __global__ void __launch_bounds__(512) quant_i8_kernel(const QuantParams p) {
     constexpr int kSteps = kQuantCached;
-    __shared__ float part[16];
+    __shared__ uint32_t part[16];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t r = WARP_ROW ? static_cast<int64_t>(blockIdx.x) * (blockDim.x >> 5) + warp : blockIdx.x;
     if (WARP_ROW && r >= p.R) return;
     const int me = WARP_ROW ? lane : threadIdx.x, all = WARP_ROW ? 32 : blockDim.x;
     QuantRaw<T, SWIGLU> raw[kSteps];
     float h[SWIGLU ? kSteps : 1][8];
-    float m = 0.0f;
+    uint32_t m = 0u;  // pattern of the largest magnitude: of T as loaded, or of SwiGLU's FP32 values
 #pragma unroll
     for (int i = 0; i < kSteps; ++i)
         if ((me + i * all) * 8 < p.K) raw[i].load(p, r, (me + i * all) * 8);
 #pragma unroll
     for (int i = 0; i < kSteps; ++i)
         if ((me + i * all) * 8 < p.K) {
-            float t[8];
-            raw[i].values(t);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                m = max_nan(m, fabsf(t[j]));
-                if constexpr (SWIGLU) h[i][j] = t[j];
+            if constexpr (SWIGLU) {
+                raw[i].values(h[i]);
+                m = most_of(m, h[i]);
+            } else {
+                m = most_bits(m, raw[i].x[0]);
             }
         }
     for (int c = (me + kSteps * all) * 8; c < p.K; c += all * 8) {
         QuantRaw<T, SWIGLU> more;
-        float t[8];
         more.load(p, r, c);
-        more.values(t);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) m = max_nan(m, fabsf(t[j]));
+        if constexpr (SWIGLU) {
+            float t[8];
+            more.values(t);
+            m = most_of(m, t);
+        } else {
+            m = most_bits(m, more.x[0]);
+        }
     }
-#pragma unroll
-    for (int off = 16; off; off >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, off));
+    m = __float_as_uint(SWIGLU ? __uint_as_float(m) : magnitude<T>(m));  // of FP32
+    m = __reduce_max_sync(0xffffffffu, m);
     if constexpr (!WARP_ROW) {
         if (lane == 0) part[warp] = m;
         __syncthreads();
         m = part[0];
-        for (int w = 1; w < static_cast<int>(blockDim.x >> 5); ++w) m = max_nan(m, part[w]);
+        for (int w = 1; w < static_cast<int>(blockDim.x >> 5); ++w) m = max(m, part[w]);
     }
-    const float s = __fdiv_rn(m, 127.0f), inv = __fdiv_rn(1.0f, s);
+    const float s = __fdiv_rn(__uint_as_float(m), 127.0f), inv = __fdiv_rn(1.0f, s);
     if (me == 0) p.scale[r] = s;
     int8_t *q = p.q + r * static_cast<int64_t>(p.K);
 #pragma unroll

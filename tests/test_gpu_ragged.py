@@ -390,6 +390,25 @@ def test_row_quantiser(R, K, dtype):
     assert torch.equal(q, codes.to(torch.int8))
 
 
+@pytest.mark.parametrize("scale", [1e-44, 1e-37, 2.0 ** -98, 1.0, 1e30, 2e38])
+def test_row_quantiser_rounds_every_quotient(scale):
+    """Rows made of the neighbourhoods of the ties: multiples of half a code and the floats beside them, for
+    scales from the subnormals to the largest; the codes are those of CUDA's own division."""
+    g = gen(77)
+    most = torch.rand(200, 1, generator=g, device="cuda") + 1.0
+    halves = torch.arange(-254, 255, device="cuda") / 2.0
+    x = (most / 127.0) * halves[None, :]
+    x = torch.cat([x, torch.nextafter(x, x + 1), torch.nextafter(x, x - 1), most, x[:, :8] * 0], dim=1) * scale
+    x = x.float()
+    q, s = bm.quant_i8_rows(x)
+    status_ok()
+    want = x.abs().amax(dim=1) / torch.full((200,), 127.0, device="cuda")
+    assert torch.equal(s, want)
+    codes = torch.round(x / want[:, None]).clamp(-127, 127)
+    codes[want == 0] = 0
+    assert torch.equal(q, codes.to(torch.int8))
+
+
 def test_quantised_rows_with_infinities_give_nan():
     g = gen(4)
     x = normal(g, 4, 64)
