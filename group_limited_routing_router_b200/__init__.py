@@ -671,6 +671,9 @@ def _rows(t, name: str, dtypes, device=None, shape=None) -> int:
 
 def _on(t, name: str, dtype, shape, device):
     """_dev of a tensor that has to be there, on `device`."""
+    if isinstance(t, torch.Tensor) and t.device == device and t.dtype is dtype and t.is_contiguous() and \
+            (shape is None or t.shape == shape):
+        return t
     if t is None:
         raise TypeError(f"{name} must be a CUDA tensor, got None")
     _dev(t, name, dtype, shape)

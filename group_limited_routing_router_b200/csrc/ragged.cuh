@@ -190,7 +190,8 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
 // Feature m (this lane; M and the lane pairing make m and m ^ 1 valid together) of rows c..c+15.  16-bit
 // outputs: neighbouring lanes exchange every other row so that each stores a pair of features.
 template <int TYPE>
-__device__ __forceinline__ void store_cols(const RaggedParams &p, const RaggedItem &it, int c, int m, const float (&v)[16]) {
+__device__ __forceinline__ void store_cols(const RaggedParams &p, const RaggedItem &it, int c, int m,
+                                           const float (&v)[16]) {
     const int lane = threadIdx.x & 31;
     if constexpr (TYPE == BEAM_MOE_F32) {
         float *o = reinterpret_cast<float *>(p.out) + (it.row0 + c) * p.ldo + m;
@@ -209,10 +210,11 @@ __device__ __forceinline__ void store_cols(const RaggedParams &p, const RaggedIt
     }
 }
 
-// The epilogue's value of an accumulator: INT8 sums take their channel's and row's scale in FP32.
+// The epilogue's value of an accumulator: INT8 sums take their channel's and then their row's scale in FP32 (in
+// this order the product of a large sum and a small scale comes first, and no product of two small ones).
 template <bool I8>
-__device__ __forceinline__ float ragged_value(const RaggedParams &p, uint32_t acc, float channel, float row) {
-    return I8 ? static_cast<float>(static_cast<int32_t>(acc)) * (channel * row) : __uint_as_float(acc);
+__device__ __forceinline__ float ragged_value(uint32_t acc, float channel, float row) {
+    return I8 ? static_cast<float>(static_cast<int32_t>(acc)) * channel * row : __uint_as_float(acc);
 }
 
 // ---- forward / dgrad on CTA pairs ------------------------------------------------------------------
@@ -227,8 +229,8 @@ __device__ __forceinline__ float ragged_value(const RaggedParams &p, uint32_t ac
 //     16-bit operands keep their short segments there) are stored chunk by chunk before TMEM goes back.
 constexpr int kRpBN = 256;
 // The rows of a k-step come in one box, of the height among eight (16, 32 .. 128 rows) that holds a CTA's half of
-// the item's rows best: several small boxes cost more than their bytes (256 groups of 128 +- 11 rows, 5120 x 2560, NA = 1: 1.42 ms
-// in boxes of 32 rows, 1.48 with a remainder of 8-row boxes, 1.32 so).
+// the item's rows best: several small boxes cost more than their bytes (256 groups of 128 +- 11 rows, 5120 x
+// 2560, NA = 1: 1.42 ms in boxes of 32 rows, 1.48 with a remainder of 8-row boxes, 1.32 so).
 constexpr int kRpBoxStep = 16, kRpBoxes = 8;
 struct RowMaps {
     CUtensorMap m[kRpBoxes];
@@ -245,7 +247,8 @@ struct RpairCfg {
     static_assert(kSmem + 128 <= 232448, "shared memory per CTA (dynamic + the 128 static bytes)");
 };
 
-// Adds `n_valid` accumulator columns of this warp's share (chunks of 16 at 16 sub + 32 i) to acc.
+// Loads (first) or adds to acc the accumulator columns of this warp's share: chunks of 16 at 16 sub + stride i,
+// those below n_valid.
 template <bool I8, int CHUNKS>
 __device__ __forceinline__ void add_segment(uint32_t t, int sub, int stride, int n_valid, bool first,
                                             uint32_t (&acc)[CHUNKS][16]) {
@@ -281,7 +284,7 @@ __device__ __forceinline__ void store_item(const RaggedParams &p, const RaggedIt
 #pragma unroll
             for (int j = 0; j < 16; ++j) {
                 const float row = (I8 && c + j < it.n_valid) ? __ldg(p.row_scale + it.row0 + c + j) : 1.0f;
-                v[j] = ragged_value<I8>(p, acc[i][j], channel, row);
+                v[j] = ragged_value<I8>(acc[i][j], channel, row);
             }
             store_cols<TYPE>(p, it, c, m, v);
         }
@@ -295,8 +298,8 @@ __device__ __forceinline__ void pack_item(const RaggedParams &p, const RaggedIte
                                           uint32_t (&pk)[2][kRpBN / 32][8]) {
 #pragma unroll
     for (int a = 0; a < 2; ++a) {
-        const float channel =
-            (I8 && m + a * kPairRows < p.M) ? __ldg(p.channel_scale + static_cast<int64_t>(it.e) * p.M + m + a * kPairRows) : 1.0f;
+        const int ma = m + a * kPairRows;
+        const float channel = (I8 && ma < p.M) ? __ldg(p.channel_scale + static_cast<int64_t>(it.e) * p.M + ma) : 1.0f;
 #pragma unroll
         for (int i = 0; i < kRpBN / 32; ++i) {
             const int c = 16 * sub + 32 * i;
@@ -309,8 +312,8 @@ __device__ __forceinline__ void pack_item(const RaggedParams &p, const RaggedIte
                     float row0 = 1.0f, row1 = 1.0f;
                     if (I8 && c + 2 * j < it.n_valid) row0 = __ldg(p.row_scale + it.row0 + c + 2 * j);
                     if (I8 && c + 2 * j + 1 < it.n_valid) row1 = __ldg(p.row_scale + it.row0 + c + 2 * j + 1);
-                    pk[a][i][j] = pack2<TYPE>(ragged_value<I8>(p, r[2 * j], channel, row0),
-                                              ragged_value<I8>(p, r[2 * j + 1], channel, row1));
+                    pk[a][i][j] = pack2<TYPE>(ragged_value<I8>(r[2 * j], channel, row0),
+                                              ragged_value<I8>(r[2 * j + 1], channel, row1));
                 }
             }
         }
@@ -318,7 +321,8 @@ __device__ __forceinline__ void pack_item(const RaggedParams &p, const RaggedIte
 }
 // NA = 2, fp32 results: each chunk is stored as it is loaded.
 template <bool I8>
-__device__ __forceinline__ void store_wide_f32(const RaggedParams &p, const RaggedItem &it, uint32_t t, int sub, int m) {
+__device__ __forceinline__ void store_wide_f32(const RaggedParams &p, const RaggedItem &it, uint32_t t, int sub,
+                                               int m) {
 #pragma unroll
     for (int a = 0; a < 2; ++a) {
         const int ma = m + a * kPairRows;
@@ -332,7 +336,7 @@ __device__ __forceinline__ void store_wide_f32(const RaggedParams &p, const Ragg
 #pragma unroll
             for (int j = 0; j < 16; ++j) {
                 const float row = (I8 && c + j < it.n_valid) ? __ldg(p.row_scale + it.row0 + c + j) : 1.0f;
-                v[j] = ragged_value<I8>(p, r[j], channel, row);
+                v[j] = ragged_value<I8>(r[j], channel, row);
             }
             store_cols<BEAM_MOE_F32>(p, it, c, ma, v);
         }
@@ -342,7 +346,8 @@ __device__ __forceinline__ void store_wide_f32(const RaggedParams &p, const Ragg
 __device__ __forceinline__ void store_packed(const RaggedParams &p, const RaggedItem &it, int sub, int m,
                                              const uint32_t (&pk)[2][kRpBN / 32][8]) {
     const int odd = threadIdx.x & 1;
-    const uint32_t sel = odd ? 0x3276u : 0x5410u;  // odd: (neighbour's high half, own), even: (own, neighbour's low half)
+    // odd lanes: (the neighbour's high half, own high half); even ones: (own low half, the neighbour's low half)
+    const uint32_t sel = odd ? 0x3276u : 0x5410u;
 #pragma unroll
     for (int a = 0; a < 2; ++a) {
         const int ma = m + a * kPairRows;
@@ -429,7 +434,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kRgThreads, 1)
                 const CUtensorMap *map_b = &tm_b.m[box - 1];
                 const int b_row = static_cast<int>(it.row0) + static_cast<int>(rank) * half;
                 const int a_row = it.mt * NA * kPairRows + static_cast<int>(rank) * kBM;
-                const uint32_t pair_bytes = 2u * static_cast<uint32_t>(NA * kRgOperand + box * kRpBoxStep * kRgRowBytes);
+                const uint32_t pair_bytes =
+                    2u * static_cast<uint32_t>(NA * kRgOperand + box * kRpBoxStep * kRgRowBytes);
                 for (int kb = 0; kb < p.n_kb; ++kb) {
                     if (!mbar_wait(&empty[stage], phase ^ 1u, p.timeout)) {
                         ok = false;
@@ -585,12 +591,17 @@ struct RsplitCfg {
 // needs a fence (plain remote stores with a cluster-scope release took about 3 us per item).
 __device__ __forceinline__ void st_async_v4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d,
                                             uint32_t bar) {
-    asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.u32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(addr),
-                 "r"(a), "r"(b), "r"(c), "r"(d), "r"(bar)
-                 : "memory");
+    asm volatile(
+        "st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.u32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(addr),
+        "r"(a), "r"(b), "r"(c), "r"(d), "r"(bar)
+        : "memory");
 }
-__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
-__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_arrive() {
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
 // Partial sums in a CTA's shared memory: [S][F = 128 / S features][BN rows], four rows (16 bytes) at a time,
 // those of feature f at place (rows / 4) ^ (f & 7), so that neighbouring features fall into different banks.
 template <int BN>
@@ -627,8 +638,9 @@ __device__ __forceinline__ void reduce_store(const RaggedParams &p, const Ragged
             const uint32_t w[4] = {sum.x, sum.y, sum.z, sum.w};
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const float row = (I8 && 4 * quad + j < it.n_valid) ? __ldg(p.row_scale + it.row0 + 4 * quad + j) : 1.0f;
-                v[j] = ragged_value<I8>(p, w[j], channel, row);
+                const int c = 4 * quad + j;
+                const float row = (I8 && c < it.n_valid) ? __ldg(p.row_scale + it.row0 + c) : 1.0f;
+                v[j] = ragged_value<I8>(w[j], channel, row);
             }
         }
         const int left = live ? it.n_valid - 4 * quad : 0;
@@ -959,9 +971,10 @@ __device__ __forceinline__ void tma_store_3d(const CUtensorMap *map, const void 
         : "memory");
 }
 __device__ __forceinline__ void tma_add_3d(const CUtensorMap *map, const void *src, int c0, int c1, int c2) {
-    asm volatile("cp.reduce.async.bulk.tensor.3d.global.shared::cta.add.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(map),
-                 "r"(c0), "r"(c1), "r"(c2), "r"(smem_u32(src))
-                 : "memory");
+    asm volatile(
+        "cp.reduce.async.bulk.tensor.3d.global.shared::cta.add.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(map),
+        "r"(c0), "r"(c1), "r"(c2), "r"(smem_u32(src))
+        : "memory");
 }
 __device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
 template <int N>
@@ -1028,8 +1041,8 @@ __device__ __forceinline__ void wgrad_store(WgradOut<BUFS> &out, int group, int 
 
 // NB = 2, 16-bit results: the two products' accumulators packed to 16 bits, TMEM handed back, then stored.
 template <int TYPE>
-__device__ __forceinline__ void wgrad_pack_store(WgradOut<1> &out, const WgradItem &it, int K, int sub, int n, bool live,
-                                                 bool rows, uint32_t t0, uint32_t acc_empty_lead) {
+__device__ __forceinline__ void wgrad_pack_store(WgradOut<1> &out, const WgradItem &it, int K, int sub, int n,
+                                                 bool live, bool rows, uint32_t t0, uint32_t acc_empty_lead) {
     uint32_t pk[2][8][8];
 #pragma unroll
     for (int b = 0; b < 2; ++b) {

@@ -601,6 +601,46 @@ def test_captured_and_replayed_with_other_groups():
     status_ok()
 
 
+def test_two_calls_at_once():
+    """Products of different kernels on two streams, overlapping: each gives what it gives alone."""
+    g = gen(61)
+    big = (normal(g, 9000, 1024), normal(g, 9000, 2048), normal(g, 4, 2048, 1024), offsets_of([3000, 1, 0, 5999]))
+    few = (normal(g, 40, 2048), normal(g, 40, 512), normal(g, 16, 512, 2048), offsets_of(ragged_counts(16, 40, 5)))
+    want = [run_all(*a, BF) for a in (big, few)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = [[], []]
+    for _ in range(8):
+        for i, a in enumerate((big, few)):
+            with torch.cuda.stream(streams[i]):
+                got[i].append(run_all(*a, BF))
+    status_ok()
+    for i in range(2):
+        for r in got[i]:
+            assert all(torch.equal(r[k], want[i][k]) for k in r)
+
+
+def test_results_past_32_bits():
+    """Outputs of more than 2^31 elements: their first and last rows, and the last expert's gradient."""
+    g = gen(71)
+    R, K, N = 270000, 64, 8192
+    x, w = normal(g, R, K), normal(g, N, K, scale=K ** -0.5)
+    out = bm.grouped_mm(x, w)
+    assert out.numel() > 2 ** 31
+    for a in (slice(0, 300), slice(R - 300, R)):
+        v = x[a].to(D) @ w.to(D).t()
+        check(out[a], v, half_step(v, BF) + sum_tol(x[a].to(D).abs() @ w.to(D).abs().t(), K, BF), "out")
+    del out
+    counts = [2] * 255 + [90]
+    dy, x = normal(g, sum(counts), 4096), normal(g, sum(counts), 4096)
+    dw = bm.grouped_mm_wgrad(dy, x, offsets_of(counts))
+    assert dw.numel() > 2 ** 31
+    for e, a, b in ((0, 0, 2), (255, 510, 600)):
+        v = dy[a:b].to(D).t() @ x[a:b].to(D)
+        check(dw[e], v, half_step(v, BF) + sum_tol(dy[a:b].to(D).abs().t() @ x[a:b].to(D).abs(), b - a, BF), f"dw {e}")
+    status_ok()
+
+
 def test_binding_refusals():
     x, w = normal(gen(1), 6, 64), normal(gen(2), 2, 32, 64)
     off = offsets_of([2, 4])
