@@ -14,7 +14,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB_DIR = os.path.join(PKG, "_lib")
 LIB = os.path.join(LIB_DIR, "libbeam_moe.so")
-MAIN = os.path.join(CSRC, "beam_moe.cu")
+MAIN = os.path.join(CSRC, "libbeam_moe.cu")
 
 NVCC_FLAGS = [
     "-O3", "-std=c++17", "-gencode", "arch=compute_100a,code=sm_100a", "-lineinfo",
@@ -24,7 +24,8 @@ NVCC_FLAGS = [
 
 
 def sources():
-    return [MAIN] + sorted(glob.glob(os.path.join(CSRC, "*.cuh"))) + [os.path.join(ROOT, "include", "beam_moe.h")]
+    return [MAIN, os.path.join(CSRC, "beam_moe.cu")] + sorted(glob.glob(os.path.join(CSRC, "*.cuh"))) + \
+        [os.path.join(ROOT, "include", "beam_moe.h")]
 
 
 def nvcc() -> str:

@@ -1198,8 +1198,8 @@ const char *beam_moe_strerror(int code) {
         case BEAM_MOE_ERR_UNSUPPORTED_DEVICE: return "unsupported device (needs compute capability 10.0, sm_100a)";
         case BEAM_MOE_ERR_CUDA: return "CUDA runtime or launch error";
         case BEAM_MOE_ERR_DEVICE_TIMEOUT: return "a bounded device-side wait timed out";
-        case BEAM_MOE_ERR_BAD_INDEX: return "an expert id outside [0, n_experts), or group offsets that do not ascend within the rows";
-        case BEAM_MOE_ERR_INVALID_ARG: return "invalid argument (a token or row count, a type or a row stride out of range)";
+        case BEAM_MOE_ERR_BAD_INDEX: return "an expert id outside [0, n_experts)";
+        case BEAM_MOE_ERR_INVALID_ARG: return "invalid argument (token count out of range)";
         default: return "unknown error code";
     }
 }
@@ -1540,7 +1540,3 @@ int beam_moe_combine(const beam_moe_config *cfg, int64_t T, const float *o_rows,
 }
 
 }  // extern "C"
-
-// ------------------------------------------------------------------------------------------------
-// The experts' products, their gradients, the INT8 products and SwiGLU as operators of their own.
-#include "ragged_api.cuh"

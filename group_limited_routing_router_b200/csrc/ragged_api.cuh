@@ -1,6 +1,6 @@
 // Host side of the grouped products, the INT8 row quantisers and SwiGLU: argument checks, tensor maps,
-// the choice of kernel, launches.  Included by beam_moe.cu, whose device set-up and tensor-map encoder it
-// uses.
+// the choice of kernel, launches.  Follows beam_moe.cu in its translation unit (libbeam_moe.cu) and uses its
+// device set-up and tensor-map encoder.
 #pragma once
 
 #include "ragged.cuh"
