@@ -81,13 +81,29 @@ __device__ __forceinline__ void umma_i8_pair(uint32_t d_tmem, uint64_t adesc, ui
         "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
         : "memory");
 }
+// Eight accumulator columns twice over (16 columns) of 16 of the warp's TMEM lanes, as 8 x 8 fragments: this
+// thread gets lane t / 4 (r[4 j], r[4 j + 1]) and lane t / 4 + 8 (r[4 j + 2], r[4 j + 3]) of columns
+// 8 j + 2 (t % 4) and the next.
+__device__ __forceinline__ void tmem_ld_frag(uint32_t taddr, uint32_t *r) {
+    asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(taddr)
+                 : "memory");
+}
+// Four 8 x 8 fragments of 16-bit values, each stored transposed: thread 8 m + i gives the address of row i (16
+// bytes) of matrix m, which receives column i of fragment m.
+__device__ __forceinline__ void stmatrix_trans(uint32_t addr, const uint32_t (&r)[4]) {
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(r[0]),
+                 "r"(r[1]), "r"(r[2]), "r"(r[3])
+                 : "memory");
+}
 __device__ __forceinline__ uint32_t idesc_with_n(uint32_t idesc, int n) {
     return idesc | (static_cast<uint32_t>(n >> 3) << 17);
 }
 
-// Arrives on a barrier of either CTA of the pair.  What is handed over is TMEM, ordered by the tcgen05 fences
-// on both sides, or this CTA's shared memory, after a proxy fence or to be overwritten: no other memory
-// operation has to be performed first, which a release at cluster scope would wait for.
+// Arrives on a barrier of any CTA of the cluster.  What is handed over is TMEM, ordered by the tcgen05 fences on
+// both sides, or shared memory, after a proxy fence or to be overwritten: no other memory operation has to be
+// performed first, which a release at cluster scope would wait for.
 __device__ __forceinline__ void mbar_arrive_async(uint32_t bar_cluster) {
     asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar_cluster) : "memory");
 }
@@ -187,29 +203,6 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
     }
 }
 
-// Feature m (this lane; M and the lane pairing make m and m ^ 1 valid together) of rows c..c+15.  16-bit
-// outputs: neighbouring lanes exchange every other row so that each stores a pair of features.
-template <int TYPE>
-__device__ __forceinline__ void store_cols(const RaggedParams &p, const RaggedItem &it, int c, int m,
-                                           const float (&v)[16]) {
-    const int lane = threadIdx.x & 31;
-    if constexpr (TYPE == BEAM_MOE_F32) {
-        float *o = reinterpret_cast<float *>(p.out) + (it.row0 + c) * p.ldo + m;
-#pragma unroll
-        for (int j = 0; j < 16; ++j)
-            if (c + j < it.n_valid && m < p.M) o[j * p.ldo] = v[j];
-    } else {
-        const int odd = lane & 1;
-        uint16_t *o = reinterpret_cast<uint16_t *>(p.out) + (it.row0 + c) * p.ldo + (m & ~1);
-#pragma unroll
-        for (int j = 0; j < 16; j += 2) {
-            const float got = __shfl_xor_sync(0xffffffffu, odd ? v[j] : v[j + 1], 1);
-            const uint32_t pr = odd ? pack2<TYPE>(got, v[j + 1]) : pack2<TYPE>(v[j], got);
-            if (c + j + odd < it.n_valid && m < p.M) *reinterpret_cast<uint32_t *>(o + (j + odd) * p.ldo) = pr;
-        }
-    }
-}
-
 // The epilogue's value of an accumulator: INT8 sums take their channel's and then their row's scale in FP32 (in
 // this order the product of a large sum and a small scale comes first, and no product of two small ones).
 template <bool I8>
@@ -217,10 +210,75 @@ __device__ __forceinline__ float ragged_value(uint32_t acc, float channel, float
     return I8 ? static_cast<float>(static_cast<int32_t>(acc)) * channel * row : __uint_as_float(acc);
 }
 
+// fp32 results: feature m (this lane) of rows c .. c + 15, 128 bytes per row and warp.
+__device__ __forceinline__ void store_cols(const RaggedParams &p, const RaggedItem &it, int c, int m,
+                                           const float (&v)[16]) {
+    float *o = reinterpret_cast<float *>(p.out) + (it.row0 + c) * p.ldo + m;
+#pragma unroll
+    for (int j = 0; j < 16; ++j)
+        if (c + j < it.n_valid && m < p.M) o[j * p.ldo] = v[j];
+}
+
+// 16-bit results.  The accumulators come as 8 x 8 fragments (tmem_ld_frag for lanes 0..15, then 16..31 of the
+// warp), are packed in pairs of rows, turned by a transposing matrix store into [row][feature] order in the
+// warp's staging buffer (64 bytes per row, 16-byte pieces swizzled by row pairs), and stored 16 bytes per lane.
+// Exchanging pairs between lanes and storing 4 bytes per lane took four times the instructions, which bound
+// products of a short contraction: 45231 rows, 224 x 4328, 241 us against @@.
+constexpr int kStage16 = 2048;  // a warp's staging: two buffers of 16 rows x 32 features
+
+// Scales of this thread's four features in the fragments of features m0 ..: m0 + t / 4 + 8 i.
+template <bool I8>
+__device__ __forceinline__ void channel_scales(const RaggedParams &p, int e, int m0, float (&ch)[4]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int m = m0 + ((threadIdx.x & 31) >> 2) + 8 * i;
+        ch[i] = (I8 && m < p.M) ? __ldg(p.channel_scale + static_cast<int64_t>(e) * p.M + m) : 1.0f;
+    }
+}
+// A chunk of 16 rows from row c on: the 16 words of its two fragment loads to 8 words of packed pairs, for
+// the two halves of 8 rows four fragments (8 features each) each.
+template <bool I8, int TYPE>
+__device__ __forceinline__ void pack_chunk(const RaggedParams &p, const RaggedItem &it, int c, const float (&ch)[4],
+                                           const uint32_t (&r)[16], uint32_t (&pk)[8]) {
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        const int row = c + 8 * j + 2 * (threadIdx.x & 3);
+        const float s0 = (I8 && row < it.n_valid) ? __ldg(p.row_scale + it.row0 + row) : 1.0f;
+        const float s1 = (I8 && row + 1 < it.n_valid) ? __ldg(p.row_scale + it.row0 + row + 1) : 1.0f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int at = 8 * (i >> 1) + 4 * j + 2 * (i & 1);
+            pk[4 * j + i] = pack2<TYPE>(ragged_value<I8>(r[at], ch[i], s0), ragged_value<I8>(r[at + 1], ch[i], s1));
+        }
+    }
+}
+// Stores a packed chunk: features m0 .. m0 + 31 (M is a multiple of 8).  `flip` alternates between the buffers, so
+// that one barrier per chunk orders a buffer's writes after the reads of two chunks ago.
+__device__ __forceinline__ void store_chunk(const RaggedParams &p, const RaggedItem &it, int c, int m0, uint32_t stage,
+                                            int flip, const uint32_t (&pk)[8]) {
+    const int lane = threadIdx.x & 31;
+    const uint32_t buf = stage + (flip & 1) * (kStage16 / 2);
+    {
+        const int row = lane & 7, m = lane >> 3;  // row of a half, fragment
+        const uint32_t at = buf + row * 64 + ((m ^ (row >> 1)) << 4);
+        stmatrix_trans(at, {pk[0], pk[1], pk[2], pk[3]});
+        stmatrix_trans(at + 512, {pk[4], pk[5], pk[6], pk[7]});
+    }
+    __syncwarp();
+    const int row = lane >> 2, piece = lane & 3;
+    const uint32_t at = buf + row * 64 + ((piece ^ ((row >> 1) & 3)) << 4);
+    const uint4 lo = lds128(at), hi = lds128(at + 512);
+    if (m0 + 8 * piece < p.M) {
+        uint16_t *o = reinterpret_cast<uint16_t *>(p.out) + (it.row0 + c + row) * p.ldo + m0 + 8 * piece;
+        if (c + row < it.n_valid) *reinterpret_cast<uint4 *>(o) = lo;
+        if (c + 8 + row < it.n_valid) *reinterpret_cast<uint4 *>(o + 8 * p.ldo) = hi;
+    }
+}
+
 // ---- forward / dgrad on CTA pairs ------------------------------------------------------------------
 // The pair engine of gemm_2sm.cuh for one product.  A pair computes NA x 256 features x up to 256 rows; CTA r
 // stages features 128 r.. of each 256 and half of the rows.
-//   NA = 1: 7 stages of 16 KB + 16 KB, two TMEM slots of 256 columns, so that a segment's or an item's
+//   NA = 1: 6 stages of 16 KB + 16 KB, two TMEM slots of 256 columns, so that a segment's or an item's
 //     epilogue always overlaps the next one's products.
 //   NA = 2: 4 stages of 2 x 16 KB + 16 KB.  The staged bytes per product fall by a quarter: with every weight
 //     met by several row tiles NA = 1 is bound by what L2 delivers to the SMs (10.5 TB/s, tensor pipe 67%
@@ -237,10 +295,11 @@ struct RowMaps {
 };
 template <int NA>
 struct RpairCfg {
-    static constexpr int kStages = NA == 1 ? 7 : 4;
+    static constexpr int kStages = NA == 1 ? 6 : 4;
     static constexpr int kStage = (NA + 1) * kRgOperand;
     static constexpr int kSlots = NA == 1 ? 2 : 1;
-    static constexpr int kBarOff = kStages * kStage;
+    static constexpr int kOutOff = kStages * kStage;  // staged 16-bit results
+    static constexpr int kBarOff = kOutOff + kGemmEpiWarps * kStage16;
     static constexpr int kTileOff = kBarOff + 256;
     static constexpr int kSmem = 1024 + kTileOff + 4 * (kPmMaxE + 1) + 64;
     static_assert(8 * (2 * kStages + 2 * kSlots + 1) + 4 <= 256, "barrier area");
@@ -248,21 +307,30 @@ struct RpairCfg {
 };
 
 // Loads (first) or adds to acc the accumulator columns of this warp's share: chunks of 16 at 16 sub + stride i,
-// those below n_valid.
-template <bool I8, int CHUNKS>
+// those below n_valid; one lane per thread, or (FRAG) as fragments.
+template <bool FRAG>
+__device__ __forceinline__ void load_chunk(uint32_t t, uint32_t (&r)[16]) {
+    if constexpr (FRAG) {
+        tmem_ld_frag(t, r);
+        tmem_ld_frag(t + (16u << 16), r + 8);
+    } else {
+        tmem_ld16(t, r);
+    }
+}
+template <bool I8, bool FRAG, int CHUNKS>
 __device__ __forceinline__ void add_segment(uint32_t t, int sub, int stride, int n_valid, bool first,
                                             uint32_t (&acc)[CHUNKS][16]) {
     if (first) {
 #pragma unroll
         for (int i = 0; i < CHUNKS; ++i)
-            if (16 * sub + stride * i < n_valid) tmem_ld16(t + 16 * sub + stride * i, acc[i]);  // warp-uniform
+            if (16 * sub + stride * i < n_valid) load_chunk<FRAG>(t + 16 * sub + stride * i, acc[i]);  // warp-uniform
         tmem_ld_wait();
     } else {
 #pragma unroll
         for (int i = 0; i < CHUNKS; ++i)
             if (16 * sub + stride * i < n_valid) {
                 uint32_t r[16];
-                tmem_ld16(t + 16 * sub + stride * i, r);
+                load_chunk<FRAG>(t + 16 * sub + stride * i, r);
                 tmem_ld_wait();
 #pragma unroll
                 for (int j = 0; j < 16; ++j)
@@ -272,49 +340,58 @@ __device__ __forceinline__ void add_segment(uint32_t t, int sub, int stride, int
     }
 }
 
+// The warp's chunks (16 sub + 32 i) of features m0 .. m0 + 31 from registers.
 template <bool I8, int TYPE, int CHUNKS>
-__device__ __forceinline__ void store_item(const RaggedParams &p, const RaggedItem &it, int sub, int m,
+__device__ __forceinline__ void store_item(const RaggedParams &p, const RaggedItem &it, int sub, int m0, uint32_t stage,
                                            const uint32_t (&acc)[CHUNKS][16]) {
-    const float channel = (I8 && m < p.M) ? __ldg(p.channel_scale + static_cast<int64_t>(it.e) * p.M + m) : 1.0f;
+    if constexpr (TYPE == BEAM_MOE_F32) {
+        const int m = m0 + (threadIdx.x & 31);
+        const float channel = (I8 && m < p.M) ? __ldg(p.channel_scale + static_cast<int64_t>(it.e) * p.M + m) : 1.0f;
 #pragma unroll
-    for (int i = 0; i < CHUNKS; ++i) {
-        const int c = 16 * sub + 32 * i;
-        if (c < it.n_valid) {  // warp-uniform
-            float v[16];
+        for (int i = 0; i < CHUNKS; ++i) {
+            const int c = 16 * sub + 32 * i;
+            if (c < it.n_valid) {  // warp-uniform
+                float v[16];
 #pragma unroll
-            for (int j = 0; j < 16; ++j) {
-                const float row = (I8 && c + j < it.n_valid) ? __ldg(p.row_scale + it.row0 + c + j) : 1.0f;
-                v[j] = ragged_value<I8>(acc[i][j], channel, row);
+                for (int j = 0; j < 16; ++j) {
+                    const float row = (I8 && c + j < it.n_valid) ? __ldg(p.row_scale + it.row0 + c + j) : 1.0f;
+                    v[j] = ragged_value<I8>(acc[i][j], channel, row);
+                }
+                store_cols(p, it, c, m, v);
             }
-            store_cols<TYPE>(p, it, c, m, v);
         }
+    } else {
+        float ch[4];
+        channel_scales<I8>(p, it.e, m0, ch);
+#pragma unroll
+        for (int i = 0; i < CHUNKS; ++i) {
+            const int c = 16 * sub + 32 * i;
+            if (c < it.n_valid) {
+                uint32_t pk[8];
+                pack_chunk<I8, TYPE>(p, it, c, ch, acc[i], pk);
+                store_chunk(p, it, c, m0, stage, i, pk);
+            }
+        }
+        __syncwarp();  // the next item starts with the first buffer again
     }
 }
 
-// NA = 2: this thread's 8 chunks of each of the item's two accumulators, packed to 16 bits: columns 2 j and
-// 2 j + 1 of chunk i of accumulator a in pk[a][i][j].
+// NA = 2: this thread's 8 chunks of each of the item's two accumulators, packed to 16 bits (pack_chunk).
 template <bool I8, int TYPE>
-__device__ __forceinline__ void pack_item(const RaggedParams &p, const RaggedItem &it, uint32_t t, int sub, int m,
+__device__ __forceinline__ void pack_item(const RaggedParams &p, const RaggedItem &it, uint32_t t, int sub, int m0,
                                           uint32_t (&pk)[2][kRpBN / 32][8]) {
 #pragma unroll
     for (int a = 0; a < 2; ++a) {
-        const int ma = m + a * kPairRows;
-        const float channel = (I8 && ma < p.M) ? __ldg(p.channel_scale + static_cast<int64_t>(it.e) * p.M + ma) : 1.0f;
+        float ch[4];
+        channel_scales<I8>(p, it.e, m0 + a * kPairRows, ch);
 #pragma unroll
         for (int i = 0; i < kRpBN / 32; ++i) {
             const int c = 16 * sub + 32 * i;
             if (c < it.n_valid) {  // warp-uniform
                 uint32_t r[16];
-                tmem_ld16(t + a * 256 + c, r);
+                load_chunk<true>(t + a * 256 + c, r);
                 tmem_ld_wait();
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    float row0 = 1.0f, row1 = 1.0f;
-                    if (I8 && c + 2 * j < it.n_valid) row0 = __ldg(p.row_scale + it.row0 + c + 2 * j);
-                    if (I8 && c + 2 * j + 1 < it.n_valid) row1 = __ldg(p.row_scale + it.row0 + c + 2 * j + 1);
-                    pk[a][i][j] = pack2<TYPE>(ragged_value<I8>(r[2 * j], channel, row0),
-                                              ragged_value<I8>(r[2 * j + 1], channel, row1));
-                }
+                pack_chunk<I8, TYPE>(p, it, c, ch, r, pk[a][i]);
             }
         }
     }
@@ -322,11 +399,11 @@ __device__ __forceinline__ void pack_item(const RaggedParams &p, const RaggedIte
 // NA = 2, fp32 results: each chunk is stored as it is loaded.
 template <bool I8>
 __device__ __forceinline__ void store_wide_f32(const RaggedParams &p, const RaggedItem &it, uint32_t t, int sub,
-                                               int m) {
+                                               int m0) {
 #pragma unroll
     for (int a = 0; a < 2; ++a) {
-        const int ma = m + a * kPairRows;
-        const float channel = (I8 && ma < p.M) ? __ldg(p.channel_scale + static_cast<int64_t>(it.e) * p.M + ma) : 1.0f;
+        const int m = m0 + a * kPairRows + (threadIdx.x & 31);
+        const float channel = (I8 && m < p.M) ? __ldg(p.channel_scale + static_cast<int64_t>(it.e) * p.M + m) : 1.0f;
 #pragma unroll 2
         for (int c = 16 * sub; c < it.n_valid; c += 32) {
             uint32_t r[16];
@@ -338,34 +415,21 @@ __device__ __forceinline__ void store_wide_f32(const RaggedParams &p, const Ragg
                 const float row = (I8 && c + j < it.n_valid) ? __ldg(p.row_scale + it.row0 + c + j) : 1.0f;
                 v[j] = ragged_value<I8>(r[j], channel, row);
             }
-            store_cols<BEAM_MOE_F32>(p, it, c, ma, v);
+            store_cols(p, it, c, m, v);
         }
     }
 }
-// Neighbouring lanes exchange words so that each stores a pair of features of one row.
-__device__ __forceinline__ void store_packed(const RaggedParams &p, const RaggedItem &it, int sub, int m,
-                                             const uint32_t (&pk)[2][kRpBN / 32][8]) {
-    const int odd = threadIdx.x & 1;
-    // odd lanes: (the neighbour's high half, own high half); even ones: (own low half, the neighbour's low half)
-    const uint32_t sel = odd ? 0x3276u : 0x5410u;
+__device__ __forceinline__ void store_packed(const RaggedParams &p, const RaggedItem &it, int sub, int m0,
+                                             uint32_t stage, const uint32_t (&pk)[2][kRpBN / 32][8]) {
 #pragma unroll
-    for (int a = 0; a < 2; ++a) {
-        const int ma = m + a * kPairRows;
-        uint16_t *o = reinterpret_cast<uint16_t *>(p.out) + (it.row0 + 16 * sub + odd) * p.ldo + (ma & ~1);
-        const int left = ma < p.M ? it.n_valid - 16 * sub - odd : 0;
+    for (int a = 0; a < 2; ++a)
 #pragma unroll
-        for (int i = 0; i < kRpBN / 32; ++i) {
-            if (16 * sub + 32 * i < it.n_valid) {  // warp-uniform
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const uint32_t got = __shfl_xor_sync(0xffffffffu, pk[a][i][j], 1);
-                    if (32 * i + 2 * j < left) *reinterpret_cast<uint32_t *>(o) = __byte_perm(pk[a][i][j], got, sel);
-                    o += 2 * p.ldo;
-                }
-                o += 16 * p.ldo;
-            }
-        }
-    }
+        for (int i = 0; i < kRpBN / 32; ++i)
+            if (16 * sub + 32 * i < it.n_valid)  // warp-uniform
+                store_chunk(p, it, 16 * sub + 32 * i, m0 + a * kPairRows, stage, i, pk[a][i]);
+            else
+                __syncwarp();  // keep the buffers' turns: the chunk that uses this one next follows a barrier
+    __syncwarp();
 }
 
 template <bool I8, bool A_MN, int NA>
@@ -524,11 +588,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kRgThreads, 1)
         const int q = warp & 3, sub = (warp - 2) / 4;
         const uint32_t acc_empty_lead = mapa_shared(smem_u32(acc_empty), 0);
         const uint32_t t0 = tmem_base + (static_cast<uint32_t>(q * 32) << 16);
+        const uint32_t stage_out = smem_u32(smem + C::kOutOff + (warp - 2) * kStage16);
         uint32_t uses = 0;
         bool ok = true;
         for (int item = pair, e = first; item < total && ok; item += n_pairs) {
             const RaggedItem it = ragged_item<kRpBN, kRound>(item, e, tile_start, p);
-            const int m = it.mt * NA * kPairRows + static_cast<int>(rank) * kBM + q * 32 + lane;
+            const int m0 = it.mt * NA * kPairRows + static_cast<int>(rank) * kBM + q * 32;
             if constexpr (NA == 1) {
                 uint32_t acc[kRpBN / 32][16];
                 for (int kb = 0; kb < p.n_kb; kb += p.seg_kb, ++uses) {
@@ -537,28 +602,33 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kRgThreads, 1)
                         break;
                     }
                     tc_fence_after();
-                    add_segment<I8, kRpBN / 32>(t0 + (uses & 1) * 256, sub, 32, it.n_valid, kb == 0, acc);
+                    const uint32_t t = t0 + (uses & 1) * 256;
+                    if (p.out_type == BEAM_MOE_F32)
+                        add_segment<I8, false, kRpBN / 32>(t, sub, 32, it.n_valid, kb == 0, acc);
+                    else
+                        add_segment<I8, true, kRpBN / 32>(t, sub, 32, it.n_valid, kb == 0, acc);
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive_async(acc_empty_lead + 8u * (uses & 1));
                 }
                 if (!ok) break;
-                if (p.out_type == BEAM_MOE_BF16) store_item<I8, BEAM_MOE_BF16, kRpBN / 32>(p, it, sub, m, acc);
-                else if (p.out_type == BEAM_MOE_F16) store_item<I8, BEAM_MOE_F16, kRpBN / 32>(p, it, sub, m, acc);
-                else store_item<I8, BEAM_MOE_F32, kRpBN / 32>(p, it, sub, m, acc);
+                if (p.out_type == BEAM_MOE_BF16) store_item<I8, BEAM_MOE_BF16, kRpBN / 32>(p, it, sub, m0, stage_out, acc);
+                else if (p.out_type == BEAM_MOE_F16)
+                    store_item<I8, BEAM_MOE_F16, kRpBN / 32>(p, it, sub, m0, stage_out, acc);
+                else store_item<I8, BEAM_MOE_F32, kRpBN / 32>(p, it, sub, m0, stage_out, acc);
             } else {
                 uint32_t pk[2][kRpBN / 32][8];
                 ok = mbar_wait(acc_full, uses & 1u, p.timeout);
                 if (!ok) break;
                 tc_fence_after();
-                if (I8 && p.out_type == BEAM_MOE_F32) store_wide_f32<I8>(p, it, t0, sub, m);
-                else if (p.out_type == BEAM_MOE_BF16) pack_item<I8, BEAM_MOE_BF16>(p, it, t0, sub, m, pk);
-                else pack_item<I8, BEAM_MOE_F16>(p, it, t0, sub, m, pk);
+                if (I8 && p.out_type == BEAM_MOE_F32) store_wide_f32<I8>(p, it, t0, sub, m0);
+                else if (p.out_type == BEAM_MOE_BF16) pack_item<I8, BEAM_MOE_BF16>(p, it, t0, sub, m0, pk);
+                else pack_item<I8, BEAM_MOE_F16>(p, it, t0, sub, m0, pk);
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive_async(acc_empty_lead);
                 ++uses;
-                if (!I8 || p.out_type != BEAM_MOE_F32) store_packed(p, it, sub, m, pk);
+                if (!I8 || p.out_type != BEAM_MOE_F32) store_packed(p, it, sub, m0, stage_out, pk);
             }
         }
     }
@@ -586,6 +656,7 @@ struct RsplitCfg {
     static constexpr int kSlot = BN < 32 ? 32 : BN;
     static_assert(8 * (2 * STAGES + 4 + 2 + 1) + 4 <= 256, "barrier area");
     static_assert(kStage % 1024 == 0 && kSmem + 128 <= 232448, "shared memory per CTA");
+    static_assert(kGemmEpiWarps * kStage16 <= BN * kBM * 4, "staged 16-bit results lie in the partial sums' place");
 };
 // 16 bytes to shared memory of a CTA of the cluster; they complete on an mbarrier of that CTA, so neither side
 // needs a fence (plain remote stores with a cluster-scope release took about 3 us per item).
@@ -824,17 +895,22 @@ __global__ void __launch_bounds__(kRgThreads, 1)
                 }
                 tc_fence_after();
                 const uint32_t t = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + (uses & 1) * C::kSlot;
-                add_segment<I8, kChunks>(t, sub, 32, it.n_valid, kb == kb0, acc);
+                if (S == 1 && p.out_type != BEAM_MOE_F32)
+                    add_segment<I8, true, kChunks>(t, sub, 32, it.n_valid, kb == kb0, acc);
+                else
+                    add_segment<I8, false, kChunks>(t, sub, 32, it.n_valid, kb == kb0, acc);
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&acc_empty[uses & 1]);
             }
             if (!ok) break;
             if (S == 1) {
-                const int m = it.mt * kBM + q * 32 + lane;
-                if (p.out_type == BEAM_MOE_BF16) store_item<I8, BEAM_MOE_BF16, kChunks>(p, it, sub, m, acc);
-                else if (p.out_type == BEAM_MOE_F16) store_item<I8, BEAM_MOE_F16, kChunks>(p, it, sub, m, acc);
-                else store_item<I8, BEAM_MOE_F32, kChunks>(p, it, sub, m, acc);
+                const int m0 = it.mt * kBM + q * 32;
+                const uint32_t stage_out = buf + (warp - 2) * kStage16;  // (no partial sums are exchanged)
+                if (p.out_type == BEAM_MOE_BF16) store_item<I8, BEAM_MOE_BF16, kChunks>(p, it, sub, m0, stage_out, acc);
+                else if (p.out_type == BEAM_MOE_F16)
+                    store_item<I8, BEAM_MOE_F16, kChunks>(p, it, sub, m0, stage_out, acc);
+                else store_item<I8, BEAM_MOE_F32, kChunks>(p, it, sub, m0, stage_out, acc);
                 continue;
             }
             if (!joined) {
@@ -1307,7 +1383,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kRwThreads, 1)
                         break;
                     }
                     tc_fence_after();
-                    add_segment<false, 8>(t0 + (uses & 1) * 256 + cols * sub, 0, 16, cols, kb == 0, acc);
+                    add_segment<false, false, 8>(t0 + (uses & 1) * 256 + cols * sub, 0, 16, cols, kb == 0, acc);
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive_async(acc_empty_lead + 8u * (uses & 1));
