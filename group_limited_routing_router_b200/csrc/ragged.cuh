@@ -172,8 +172,14 @@ struct RaggedItem {
     int once;  // the group has one row tile, so its weights are read once: L2 evict-first
     int64_t row0;
 };
+// Bands of 8 row tiles go over all feature tiles in turn, so that what runs at one time reads some 8 row tiles and
+// 9 feature tiles of 256; with all row tiles of a feature tile first it is 75 tiles, and the rows of a long group
+// come from HBM for each feature tile (bf16, NA = 1: 16384 rows, 5120 x 2048, 271 -> 237 us; 32768 rows, 2048 x
+// 4096, 418 -> 354; bands of 4 and 16 measure alike, of 32 1 to 3% more).
+constexpr int kBandTiles = 8;
 template <int BN, int ROUND>
-__device__ __forceinline__ RaggedItem ragged_item(int item, int &e, const int *tile_start, const RaggedParams &p) {
+__device__ __forceinline__ RaggedItem ragged_item(int item, int &e, int n_mt, const int *tile_start,
+                                                  const RaggedParams &p) {
     RaggedItem it;
     while (tile_start[e + 1] <= item) ++e;
     it.e = e;
@@ -181,8 +187,14 @@ __device__ __forceinline__ RaggedItem ragged_item(int item, int &e, const int *t
     const int n_nt = (rows + BN - 1) / BN;
     const int per = n_nt == 1 ? (rows + ROUND - 1) / ROUND * ROUND : tile_rows<BN, ROUND>(rows);
     const int local = item - tile_start[e];
-    it.mt = n_nt == 1 ? local : local / n_nt;
-    const int nt = local - it.mt * n_nt;
+    int nt = 0;
+    it.mt = local;
+    if (n_nt > 1) {
+        const int band = local / (kBandTiles * n_mt), left = local - band * kBandTiles * n_mt;
+        const int tiles = min(kBandTiles, n_nt - band * kBandTiles);
+        it.mt = left / tiles;
+        nt = band * kBandTiles + left - it.mt * tiles;
+    }
     it.n_valid = min(per, rows - nt * per);  // > 0: rows > BN (n_nt - 1) >= per (n_nt - 1)
     it.n_mma = (it.n_valid + ROUND - 1) / ROUND * ROUND;
     it.once = n_nt == 1;
@@ -220,11 +232,16 @@ __device__ __forceinline__ void store_cols(const RaggedParams &p, const RaggedIt
 }
 
 // 16-bit results.  The accumulators come as 8 x 8 fragments (tmem_ld_frag for lanes 0..15, then 16..31 of the
-// warp), are packed in pairs of rows, turned by a transposing matrix store into [row][feature] order in the
-// warp's staging buffer (64 bytes per row, 16-byte pieces swizzled by row pairs), and stored 16 bytes per lane.
-// Exchanging pairs between lanes and storing 4 bytes per lane took four times the instructions, which bound
-// products of a short contraction: 45231 rows, 224 x 4328, 241 us against @@.
-constexpr int kStage16 = 2048;  // a warp's staging: two buffers of 16 rows x 32 features
+// warp), are packed in pairs of rows, and are turned by a transposing matrix store into [row][feature] order in a
+// staging buffer that the four warps of a chunk's 128 features share, so that each store instruction covers two
+// whole rows of 256 bytes.  45231 rows, 224 x 4328: 141 us (filling the result alone takes 100 to 120); 219 with
+// 64 bytes per row and warp, 241 with pairs exchanged between lanes and 4 bytes stored per lane.
+constexpr int kStage16 = 4096;  // a staging buffer: 16 rows x 128 features
+constexpr int kStage16All = 4 * kStage16;  // two per group of four warps
+
+// The four epilogue warps that share a chunk (`sub` 0 or 1).  They run the same chunks of the same items, after a
+// wait that has timed out too.
+__device__ __forceinline__ void quad_sync(int sub) { asm volatile("bar.sync %0, 128;" ::"r"(1 + sub) : "memory"); }
 
 // Scales of this thread's four features in the fragments of features m0 ..: m0 + t / 4 + 8 i.
 template <bool I8>
@@ -235,16 +252,27 @@ __device__ __forceinline__ void channel_scales(const RaggedParams &p, int e, int
         ch[i] = (I8 && m < p.M) ? __ldg(p.channel_scale + static_cast<int64_t>(e) * p.M + m) : 1.0f;
     }
 }
-// A chunk of 16 rows from row c on: the 16 words of its two fragment loads to 8 words of packed pairs, for
-// the two halves of 8 rows four fragments (8 features each) each.
+// Scales of the item's rows, 32 i + lane, asked for before its sums are waited for: they would cost every chunk
+// a trip to memory (48222 rows, 128 x 2112, INT8: 193 us so, 151 ahead of the wait).
+template <bool I8, int CHUNKS>
+__device__ __forceinline__ void row_scales(const RaggedParams &p, const RaggedItem &it, float (&rs)[CHUNKS]) {
+#pragma unroll
+    for (int i = 0; i < CHUNKS; ++i) {
+        const int row = 32 * i + (threadIdx.x & 31);
+        rs[i] = (I8 && row < it.n_valid) ? __ldg(p.row_scale + it.row0 + row) : 1.0f;
+    }
+}
+// A chunk of 16 rows: the 16 words of its two fragment loads to 8 words of packed pairs, for the two halves of 8
+// rows four fragments (8 features each) each.  rs: the scales of its 32 rows (row_scales), of which it is the
+// half `sub`.
 template <bool I8, int TYPE>
-__device__ __forceinline__ void pack_chunk(const RaggedParams &p, const RaggedItem &it, int c, const float (&ch)[4],
-                                           const uint32_t (&r)[16], uint32_t (&pk)[8]) {
+__device__ __forceinline__ void pack_chunk(int sub, float rs, const float (&ch)[4], const uint32_t (&r)[16],
+                                           uint32_t (&pk)[8]) {
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-        const int row = c + 8 * j + 2 * (threadIdx.x & 3);
-        const float s0 = (I8 && row < it.n_valid) ? __ldg(p.row_scale + it.row0 + row) : 1.0f;
-        const float s1 = (I8 && row + 1 < it.n_valid) ? __ldg(p.row_scale + it.row0 + row + 1) : 1.0f;
+        const int row = 16 * sub + 8 * j + 2 * (threadIdx.x & 3);
+        const float s0 = I8 ? __shfl_sync(0xffffffffu, rs, row) : 1.0f;
+        const float s1 = I8 ? __shfl_sync(0xffffffffu, rs, row + 1) : 1.0f;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int at = 8 * (i >> 1) + 4 * j + 2 * (i & 1);
@@ -252,26 +280,27 @@ __device__ __forceinline__ void pack_chunk(const RaggedParams &p, const RaggedIt
         }
     }
 }
-// Stores a packed chunk: features m0 .. m0 + 31 (M is a multiple of 8).  `flip` alternates between the buffers, so
-// that one barrier per chunk orders a buffer's writes after the reads of two chunks ago.
-__device__ __forceinline__ void store_chunk(const RaggedParams &p, const RaggedItem &it, int c, int m0, uint32_t stage,
-                                            int flip, const uint32_t (&pk)[8]) {
+// Stores a packed chunk of 16 rows from row c on.  q: this warp's 32 of the 128 features from mt0 on (M is a
+// multiple of 8); stage: its four warps' two buffers, between which `flip` alternates, so that one barrier per
+// chunk orders a buffer's writes after the reads of two chunks ago.  live: false after a wait has timed out.
+__device__ __forceinline__ void store_chunk(const RaggedParams &p, const RaggedItem &it, int c, int mt0, int q, int sub,
+                                            uint32_t stage, int flip, bool live, const uint32_t (&pk)[8]) {
     const int lane = threadIdx.x & 31;
-    const uint32_t buf = stage + (flip & 1) * (kStage16 / 2);
+    const uint32_t buf = stage + (flip & 1) * kStage16;
     {
-        const int row = lane & 7, m = lane >> 3;  // row of a half, fragment
-        const uint32_t at = buf + row * 64 + ((m ^ (row >> 1)) << 4);
+        const int row = lane & 7, piece = 4 * q + (lane >> 3);  // row of a half, 16-byte piece of the row
+        const uint32_t at = buf + row * 256 + ((piece ^ row) << 4);
         stmatrix_trans(at, {pk[0], pk[1], pk[2], pk[3]});
-        stmatrix_trans(at + 512, {pk[4], pk[5], pk[6], pk[7]});
+        stmatrix_trans(at + 8 * 256, {pk[4], pk[5], pk[6], pk[7]});
     }
-    __syncwarp();
-    const int row = lane >> 2, piece = lane & 3;
-    const uint32_t at = buf + row * 64 + ((piece ^ ((row >> 1) & 3)) << 4);
-    const uint4 lo = lds128(at), hi = lds128(at + 512);
-    if (m0 + 8 * piece < p.M) {
-        uint16_t *o = reinterpret_cast<uint16_t *>(p.out) + (it.row0 + c + row) * p.ldo + m0 + 8 * piece;
+    quad_sync(sub);
+    const int row = 4 * q + (lane >> 4), piece = lane & 15;  // rows 4 q, 4 q + 1, then the next two
+    const uint32_t at = buf + row * 256;
+    const uint4 lo = lds128(at + ((piece ^ (row & 7)) << 4)), hi = lds128(at + 512 + ((piece ^ ((row + 2) & 7)) << 4));
+    if (live && mt0 + 8 * piece < p.M) {
+        uint16_t *o = reinterpret_cast<uint16_t *>(p.out) + (it.row0 + c + row) * p.ldo + mt0 + 8 * piece;
         if (c + row < it.n_valid) *reinterpret_cast<uint4 *>(o) = lo;
-        if (c + 8 + row < it.n_valid) *reinterpret_cast<uint4 *>(o + 8 * p.ldo) = hi;
+        if (c + row + 2 < it.n_valid) *reinterpret_cast<uint4 *>(o + 2 * p.ldo) = hi;
     }
 }
 
@@ -279,12 +308,13 @@ __device__ __forceinline__ void store_chunk(const RaggedParams &p, const RaggedI
 // The pair engine of gemm_2sm.cuh for one product.  A pair computes NA x 256 features x up to 256 rows; CTA r
 // stages features 128 r.. of each 256 and half of the rows.
 //   NA = 1: 6 stages of 16 KB + 16 KB, two TMEM slots of 256 columns, so that a segment's or an item's
-//     epilogue always overlaps the next one's products.
-//   NA = 2: 4 stages of 2 x 16 KB + 16 KB.  The staged bytes per product fall by a quarter: with every weight
-//     met by several row tiles NA = 1 is bound by what L2 delivers to the SMs (10.5 TB/s, tensor pipe 67%
-//     busy, bf16 and INT8 alike taking 0.47 us per k-step).  Its one item fills TMEM, so the epilogue packs
-//     the accumulators to 16 bits in registers, hands TMEM back and then stores; fp32 results (of INT8 only:
-//     16-bit operands keep their short segments there) are stored chunk by chunk before TMEM goes back.
+//     epilogue always overlaps the next one's products.  INT8 sums are one segment: packed to 16 bits as they are
+//     loaded (48222 rows, 128 x 2112: 151 us held as 32-bit words first, 107 so), or stored chunk by chunk (fp32).
+//   NA = 2, 16-bit operands and results: 4 stages of 2 x 16 KB + 16 KB.  The staged bytes per product fall by a
+//     quarter, for products that are bound by what L2 delivers to the SMs (ragged_plan).  Its one item fills TMEM,
+//     so the epilogue packs the accumulators to 16 bits in registers, hands TMEM back and then stores.  INT8, whose
+//     k-steps hold twice the products, has no such kernel: 8192 rows, 5120 x 5120, 131 us with NA = 1, 156 with 2;
+//     8192 rows, 8192 x 8192, 340 and 346.
 constexpr int kRpBN = 256;
 // The rows of a k-step come in one box, of the height among eight (16, 32 .. 128 rows) that holds a CTA's half of
 // the item's rows best: several small boxes cost more than their bytes (256 groups of 128 +- 11 rows, 5120 x
@@ -299,7 +329,7 @@ struct RpairCfg {
     static constexpr int kStage = (NA + 1) * kRgOperand;
     static constexpr int kSlots = NA == 1 ? 2 : 1;
     static constexpr int kOutOff = kStages * kStage;  // staged 16-bit results
-    static constexpr int kBarOff = kOutOff + kGemmEpiWarps * kStage16;
+    static constexpr int kBarOff = kOutOff + kStage16All;
     static constexpr int kTileOff = kBarOff + 256;
     static constexpr int kSmem = 1024 + kTileOff + 4 * (kPmMaxE + 1) + 64;
     static_assert(8 * (2 * kStages + 2 * kSlots + 1) + 4 <= 256, "barrier area");
@@ -340,12 +370,13 @@ __device__ __forceinline__ void add_segment(uint32_t t, int sub, int stride, int
     }
 }
 
-// The warp's chunks (16 sub + 32 i) of features m0 .. m0 + 31 from registers.
+// The warp's chunks (16 sub + 32 i) of its 32 features (mt0 + 32 q ..) from registers.
 template <bool I8, int TYPE, int CHUNKS>
-__device__ __forceinline__ void store_item(const RaggedParams &p, const RaggedItem &it, int sub, int m0, uint32_t stage,
+__device__ __forceinline__ void store_item(const RaggedParams &p, const RaggedItem &it, int sub, int q, int mt0,
+                                           uint32_t stage, bool live, const float (&rs)[CHUNKS],
                                            const uint32_t (&acc)[CHUNKS][16]) {
     if constexpr (TYPE == BEAM_MOE_F32) {
-        const int m = m0 + (threadIdx.x & 31);
+        const int m = mt0 + 32 * q + (threadIdx.x & 31);
         const float channel = (I8 && m < p.M) ? __ldg(p.channel_scale + static_cast<int64_t>(it.e) * p.M + m) : 1.0f;
 #pragma unroll
         for (int i = 0; i < CHUNKS; ++i) {
@@ -353,37 +384,35 @@ __device__ __forceinline__ void store_item(const RaggedParams &p, const RaggedIt
             if (c < it.n_valid) {  // warp-uniform
                 float v[16];
 #pragma unroll
-                for (int j = 0; j < 16; ++j) {
-                    const float row = (I8 && c + j < it.n_valid) ? __ldg(p.row_scale + it.row0 + c + j) : 1.0f;
-                    v[j] = ragged_value<I8>(acc[i][j], channel, row);
-                }
-                store_cols(p, it, c, m, v);
+                for (int j = 0; j < 16; ++j)
+                    v[j] = ragged_value<I8>(acc[i][j], channel,
+                                            I8 ? __shfl_sync(0xffffffffu, rs[i], 16 * sub + j) : 1.0f);
+                if (live) store_cols(p, it, c, m, v);
             }
         }
     } else {
         float ch[4];
-        channel_scales<I8>(p, it.e, m0, ch);
+        channel_scales<I8>(p, it.e, mt0 + 32 * q, ch);
 #pragma unroll
         for (int i = 0; i < CHUNKS; ++i) {
             const int c = 16 * sub + 32 * i;
-            if (c < it.n_valid) {
+            if (c < it.n_valid) {  // the same for the four warps
                 uint32_t pk[8];
-                pack_chunk<I8, TYPE>(p, it, c, ch, acc[i], pk);
-                store_chunk(p, it, c, m0, stage, i, pk);
+                pack_chunk<I8, TYPE>(sub, rs[i], ch, acc[i], pk);
+                store_chunk(p, it, c, mt0, q, sub, stage, i, live, pk);
             }
         }
-        __syncwarp();  // the next item starts with the first buffer again
+        quad_sync(sub);  // the next item starts with the first buffer again
     }
 }
 
-// NA = 2: this thread's 8 chunks of each of the item's two accumulators, packed to 16 bits (pack_chunk).
-template <bool I8, int TYPE>
-__device__ __forceinline__ void pack_item(const RaggedParams &p, const RaggedItem &it, uint32_t t, int sub, int m0,
-                                          uint32_t (&pk)[2][kRpBN / 32][8]) {
+// Items of one segment (NA = 2; INT8): this thread's 8 chunks of each of the item's NA accumulators, packed to 16
+// bits (pack_chunk).
+template <bool I8, int TYPE, int NA>
+__device__ __forceinline__ void pack_item(const RaggedItem &it, uint32_t t, int sub, const float (&rs)[kRpBN / 32],
+                                          const float (&ch)[NA][4], uint32_t (&pk)[NA][kRpBN / 32][8]) {
 #pragma unroll
-    for (int a = 0; a < 2; ++a) {
-        float ch[4];
-        channel_scales<I8>(p, it.e, m0 + a * kPairRows, ch);
+    for (int a = 0; a < NA; ++a) {
 #pragma unroll
         for (int i = 0; i < kRpBN / 32; ++i) {
             const int c = 16 * sub + 32 * i;
@@ -391,45 +420,42 @@ __device__ __forceinline__ void pack_item(const RaggedParams &p, const RaggedIte
                 uint32_t r[16];
                 load_chunk<true>(t + a * 256 + c, r);
                 tmem_ld_wait();
-                pack_chunk<I8, TYPE>(p, it, c, ch, r, pk[a][i]);
+                pack_chunk<I8, TYPE>(sub, rs[i], ch[a], r, pk[a][i]);
             }
         }
     }
 }
-// NA = 2, fp32 results: each chunk is stored as it is loaded.
-template <bool I8>
-__device__ __forceinline__ void store_wide_f32(const RaggedParams &p, const RaggedItem &it, uint32_t t, int sub,
-                                               int m0) {
+// INT8's fp32 results: each chunk is stored as it is loaded.
+__device__ __forceinline__ void store_i8_f32(const RaggedParams &p, const RaggedItem &it, uint32_t t, int sub, int m0,
+                                             bool live, const float (&rs)[kRpBN / 32]) {
+    const int m = m0 + (threadIdx.x & 31);
+    const float channel = m < p.M ? __ldg(p.channel_scale + static_cast<int64_t>(it.e) * p.M + m) : 1.0f;
 #pragma unroll
-    for (int a = 0; a < 2; ++a) {
-        const int m = m0 + a * kPairRows + (threadIdx.x & 31);
-        const float channel = (I8 && m < p.M) ? __ldg(p.channel_scale + static_cast<int64_t>(it.e) * p.M + m) : 1.0f;
-#pragma unroll 2
-        for (int c = 16 * sub; c < it.n_valid; c += 32) {
+    for (int i = 0; i < kRpBN / 32; ++i) {
+        const int c = 16 * sub + 32 * i;
+        if (c < it.n_valid) {  // warp-uniform
             uint32_t r[16];
-            tmem_ld16(t + a * 256 + c, r);
+            tmem_ld16(t + c, r);
             tmem_ld_wait();
             float v[16];
 #pragma unroll
-            for (int j = 0; j < 16; ++j) {
-                const float row = (I8 && c + j < it.n_valid) ? __ldg(p.row_scale + it.row0 + c + j) : 1.0f;
-                v[j] = ragged_value<I8>(r[j], channel, row);
-            }
-            store_cols(p, it, c, m, v);
+            for (int j = 0; j < 16; ++j)
+                v[j] = ragged_value<true>(r[j], channel, __shfl_sync(0xffffffffu, rs[i], 16 * sub + j));
+            if (live) store_cols(p, it, c, m, v);
         }
     }
 }
-__device__ __forceinline__ void store_packed(const RaggedParams &p, const RaggedItem &it, int sub, int m0,
-                                             uint32_t stage, const uint32_t (&pk)[2][kRpBN / 32][8]) {
+template <int NA>
+__device__ __forceinline__ void store_packed(const RaggedParams &p, const RaggedItem &it, int sub, int q, int mt0,
+                                             uint32_t stage, bool live, const uint32_t (&pk)[NA][kRpBN / 32][8]) {
 #pragma unroll
-    for (int a = 0; a < 2; ++a)
+    for (int a = 0; a < NA; ++a) {
 #pragma unroll
         for (int i = 0; i < kRpBN / 32; ++i)
-            if (16 * sub + 32 * i < it.n_valid)  // warp-uniform
-                store_chunk(p, it, 16 * sub + 32 * i, m0 + a * kPairRows, stage, i, pk[a][i]);
-            else
-                __syncwarp();  // keep the buffers' turns: the chunk that uses this one next follows a barrier
-    __syncwarp();
+            if (16 * sub + 32 * i < it.n_valid)  // the same for the four warps
+                store_chunk(p, it, 16 * sub + 32 * i, mt0 + a * kPairRows, q, sub, stage, i, live, pk[a][i]);
+        quad_sync(sub);  // the buffers' turns start over
+    }
 }
 
 template <bool I8, bool A_MN, int NA>
@@ -437,6 +463,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kRgThreads, 1)
     ragged_pair_kernel(const __grid_constant__ CUtensorMap tm_w,  // weights [E][N][K]
                        const __grid_constant__ RowMaps tm_b,      // rows [R][contraction], by box height
                        const RaggedParams p) {
+    static_assert(NA == 1 || !I8, "INT8 runs with NA = 1");
     using C = RpairCfg<NA>;
     constexpr int kRound = I8 ? 32 : 16;
     constexpr int kStages = C::kStages;
@@ -491,7 +518,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kRgThreads, 1)
             uint32_t phase = 0, issued = 0, issued_phase = 0;
             bool ok = true;
             for (int item = pair, e = first; item < total && ok; item += n_pairs) {
-                const RaggedItem it = ragged_item<kRpBN, kRound>(item, e, tile_start, p);
+                const RaggedItem it = ragged_item<kRpBN, kRound>(item, e, n_mt, tile_start, p);
                 const uint64_t pol_w = it.once ? pol_once : pol_again;
                 const int half = it.n_mma / 2;
                 const int box = (half + kRpBoxStep - 1) / kRpBoxStep;  // 1..8
@@ -539,7 +566,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kRgThreads, 1)
             uint32_t phase = 0, uses = 0;
             bool ok = true;
             for (int item = pair, e = first; item < total && ok; item += n_pairs) {
-                const RaggedItem it = ragged_item<kRpBN, kRound>(item, e, tile_start, p);
+                const RaggedItem it = ragged_item<kRpBN, kRound>(item, e, n_mt, tile_start, p);
                 const uint32_t idesc = idesc_with_n(p.idesc, it.n_mma);
                 for (int kb = 0; kb < p.n_kb && ok;) {
                     const int seg_end = NA == 1 ? min(p.n_kb, kb + p.seg_kb) : p.n_kb;
@@ -588,19 +615,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kRgThreads, 1)
         const int q = warp & 3, sub = (warp - 2) / 4;
         const uint32_t acc_empty_lead = mapa_shared(smem_u32(acc_empty), 0);
         const uint32_t t0 = tmem_base + (static_cast<uint32_t>(q * 32) << 16);
-        const uint32_t stage_out = smem_u32(smem + C::kOutOff + (warp - 2) * kStage16);
+        const uint32_t stage_out = smem_u32(smem + C::kOutOff) + 2 * sub * kStage16;
         uint32_t uses = 0;
-        bool ok = true;
-        for (int item = pair, e = first; item < total && ok; item += n_pairs) {
-            const RaggedItem it = ragged_item<kRpBN, kRound>(item, e, tile_start, p);
-            const int m0 = it.mt * NA * kPairRows + static_cast<int>(rank) * kBM + q * 32;
-            if constexpr (NA == 1) {
+        bool ok = true;  // (the four warps of a quad stay together after a wait has timed out)
+        for (int item = pair, e = first; item < total; item += n_pairs) {
+            const RaggedItem it = ragged_item<kRpBN, kRound>(item, e, n_mt, tile_start, p);
+            const int mt0 = it.mt * NA * kPairRows + static_cast<int>(rank) * kBM;  // this CTA's 128 features
+            float rs[kRpBN / 32];
+            row_scales<I8>(p, it, rs);
+            if constexpr (NA == 1 && !I8) {
                 uint32_t acc[kRpBN / 32][16];
                 for (int kb = 0; kb < p.n_kb; kb += p.seg_kb, ++uses) {
-                    if (!mbar_wait(&acc_full[uses & 1], (uses >> 1) & 1u, p.timeout)) {
-                        ok = false;
-                        break;
-                    }
+                    ok = ok && mbar_wait(&acc_full[uses & 1], (uses >> 1) & 1u, p.timeout);
                     tc_fence_after();
                     const uint32_t t = t0 + (uses & 1) * 256;
                     if (p.out_type == BEAM_MOE_F32)
@@ -611,24 +637,32 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kRgThreads, 1)
                     __syncwarp();
                     if (lane == 0) mbar_arrive_async(acc_empty_lead + 8u * (uses & 1));
                 }
-                if (!ok) break;
-                if (p.out_type == BEAM_MOE_BF16) store_item<I8, BEAM_MOE_BF16, kRpBN / 32>(p, it, sub, m0, stage_out, acc);
+                if (p.out_type == BEAM_MOE_BF16)
+                    store_item<I8, BEAM_MOE_BF16, kRpBN / 32>(p, it, sub, q, mt0, stage_out, ok, rs, acc);
                 else if (p.out_type == BEAM_MOE_F16)
-                    store_item<I8, BEAM_MOE_F16, kRpBN / 32>(p, it, sub, m0, stage_out, acc);
-                else store_item<I8, BEAM_MOE_F32, kRpBN / 32>(p, it, sub, m0, stage_out, acc);
+                    store_item<I8, BEAM_MOE_F16, kRpBN / 32>(p, it, sub, q, mt0, stage_out, ok, rs, acc);
+                else
+                    store_item<I8, BEAM_MOE_F32, kRpBN / 32>(p, it, sub, q, mt0, stage_out, ok, rs, acc);
             } else {
-                uint32_t pk[2][kRpBN / 32][8];
-                ok = mbar_wait(acc_full, uses & 1u, p.timeout);
-                if (!ok) break;
+                uint32_t pk[NA][kRpBN / 32][8];
+                float ch[NA][4];
+#pragma unroll
+                for (int a = 0; a < NA; ++a) channel_scales<I8>(p, it.e, mt0 + 32 * q + a * kPairRows, ch[a]);
+                const uint32_t slot = uses % C::kSlots, t = t0 + slot * 256;
+                ok = ok && mbar_wait(&acc_full[slot], (uses / C::kSlots) & 1u, p.timeout);
                 tc_fence_after();
-                if (I8 && p.out_type == BEAM_MOE_F32) store_wide_f32<I8>(p, it, t0, sub, m0);
-                else if (p.out_type == BEAM_MOE_BF16) pack_item<I8, BEAM_MOE_BF16>(p, it, t0, sub, m0, pk);
-                else pack_item<I8, BEAM_MOE_F16>(p, it, t0, sub, m0, pk);
+                if (I8 && p.out_type == BEAM_MOE_F32) {
+                    store_i8_f32(p, it, t, sub, mt0 + 32 * q, ok, rs);
+                } else if (p.out_type == BEAM_MOE_BF16) {
+                    pack_item<I8, BEAM_MOE_BF16, NA>(it, t, sub, rs, ch, pk);
+                } else {
+                    pack_item<I8, BEAM_MOE_F16, NA>(it, t, sub, rs, ch, pk);
+                }
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive_async(acc_empty_lead);
+                if (lane == 0) mbar_arrive_async(acc_empty_lead + 8u * slot);
                 ++uses;
-                if (!I8 || p.out_type != BEAM_MOE_F32) store_packed(p, it, sub, m0, stage_out, pk);
+                if (!I8 || p.out_type != BEAM_MOE_F32) store_packed<NA>(p, it, sub, q, mt0, stage_out, ok, pk);
             }
         }
     }
@@ -656,7 +690,7 @@ struct RsplitCfg {
     static constexpr int kSlot = BN < 32 ? 32 : BN;
     static_assert(8 * (2 * STAGES + 4 + 2 + 1) + 4 <= 256, "barrier area");
     static_assert(kStage % 1024 == 0 && kSmem + 128 <= 232448, "shared memory per CTA");
-    static_assert(kGemmEpiWarps * kStage16 <= BN * kBM * 4, "staged 16-bit results lie in the partial sums' place");
+    static_assert(kStage16All <= BN * kBM * 4, "staged 16-bit results lie in the partial sums' place");
 };
 // 16 bytes to shared memory of a CTA of the cluster; they complete on an mbarrier of that CTA, so neither side
 // needs a fence (plain remote stores with a cluster-scope release took about 3 us per item).
@@ -798,7 +832,7 @@ __global__ void __launch_bounds__(kRgThreads, 1)
             uint32_t phase = 0, issued = 0, issued_phase = 0;
             bool ok = true;
             for (int item = cluster, e = first; item < total && ok; item += n_clusters) {
-                const RaggedItem it = ragged_item<BN, 16>(item, e, tile_start, p);
+                const RaggedItem it = ragged_item<BN, 16>(item, e, n_mt, tile_start, p);
                 const uint64_t pol_w = it.once ? pol_once : pol_again;
                 const int nbox = (it.n_mma + C::kBox - 1) / C::kBox;
                 const int a_row = it.mt * kBM;
@@ -836,7 +870,7 @@ __global__ void __launch_bounds__(kRgThreads, 1)
             uint32_t phase = 0, uses = 0;
             bool ok = true;
             for (int item = cluster, e = first; item < total && ok; item += n_clusters) {
-                const RaggedItem it = ragged_item<BN, 16>(item, e, tile_start, p);
+                const RaggedItem it = ragged_item<BN, 16>(item, e, n_mt, tile_start, p);
                 const uint32_t idesc = idesc_with_n(p.idesc, it.n_mma);
                 for (int kb = kb0; kb < kb1 && ok;) {
                     const int seg_end = min(kb1, kb + p.seg_kb);
@@ -885,14 +919,13 @@ __global__ void __launch_bounds__(kRgThreads, 1)
         const uint32_t push = mapa_shared(buf, dst), push_bar = mapa_shared(smem_u32(red_full), dst);
         uint32_t uses = 0, n_item = 0;
         bool ok = true, joined = false;  // joined: the other CTAs' barriers are known to be initialised
-        for (int item = cluster, e = first; item < total && ok; item += n_clusters, ++n_item) {
-            const RaggedItem it = ragged_item<BN, 16>(item, e, tile_start, p);
+        for (int item = cluster, e = first; item < total; item += n_clusters, ++n_item) {
+            const RaggedItem it = ragged_item<BN, 16>(item, e, n_mt, tile_start, p);
             uint32_t acc[kChunks][16];
+            float rs[kChunks];
+            if (S == 1) row_scales<I8>(p, it, rs);
             for (int kb = kb0; kb < kb1; kb += p.seg_kb, ++uses) {
-                if (!mbar_wait(&acc_full[uses & 1], (uses >> 1) & 1u, p.timeout)) {
-                    ok = false;
-                    break;
-                }
+                ok = ok && mbar_wait(&acc_full[uses & 1], (uses >> 1) & 1u, p.timeout);
                 tc_fence_after();
                 const uint32_t t = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + (uses & 1) * C::kSlot;
                 if (S == 1 && p.out_type != BEAM_MOE_F32)
@@ -903,16 +936,17 @@ __global__ void __launch_bounds__(kRgThreads, 1)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&acc_empty[uses & 1]);
             }
-            if (!ok) break;
-            if (S == 1) {
-                const int m0 = it.mt * kBM + q * 32;
-                const uint32_t stage_out = buf + (warp - 2) * kStage16;  // (no partial sums are exchanged)
-                if (p.out_type == BEAM_MOE_BF16) store_item<I8, BEAM_MOE_BF16, kChunks>(p, it, sub, m0, stage_out, acc);
+            if (S == 1) {  // (the four warps of a quad stay together after a wait has timed out)
+                const uint32_t stage_out = buf + 2 * sub * kStage16;  // (no partial sums are exchanged)
+                if (p.out_type == BEAM_MOE_BF16)
+                    store_item<I8, BEAM_MOE_BF16, kChunks>(p, it, sub, q, it.mt * kBM, stage_out, ok, rs, acc);
                 else if (p.out_type == BEAM_MOE_F16)
-                    store_item<I8, BEAM_MOE_F16, kChunks>(p, it, sub, m0, stage_out, acc);
-                else store_item<I8, BEAM_MOE_F32, kChunks>(p, it, sub, m0, stage_out, acc);
+                    store_item<I8, BEAM_MOE_F16, kChunks>(p, it, sub, q, it.mt * kBM, stage_out, ok, rs, acc);
+                else
+                    store_item<I8, BEAM_MOE_F32, kChunks>(p, it, sub, q, it.mt * kBM, stage_out, ok, rs, acc);
                 continue;
             }
+            if (!ok) break;
             if (!joined) {
                 cluster_wait();
                 joined = true;

@@ -45,8 +45,9 @@ bool set_smem(F *kernel, int bytes) {
 template <int NA>
 bool set_pair_smem() {
     constexpr int n = RpairCfg<NA>::kSmem;
-    return set_smem(ragged_pair_kernel<false, false, NA>, n) && set_smem(ragged_pair_kernel<false, true, NA>, n) &&
-           set_smem(ragged_pair_kernel<true, false, NA>, n);
+    if constexpr (NA == 1)
+        if (!set_smem(ragged_pair_kernel<true, false, NA>, n)) return false;
+    return set_smem(ragged_pair_kernel<false, false, NA>, n) && set_smem(ragged_pair_kernel<false, true, NA>, n);
 }
 template <int BN, int ST>
 bool set_split_smem() {
@@ -176,14 +177,10 @@ int launch_split_any(bool i8, bool a_mn, int S, int clusters, cudaStream_t s, co
     return launch_split<false, false, BN, ST>(S, clusters, s, w, b, p);
 }
 
-template <int NA>
-int launch_pair(bool i8, bool a_mn, int pairs, cudaStream_t s, const CUtensorMap &w, const RowMaps &b,
-                const RaggedParams &p) {
-    constexpr int n = RpairCfg<NA>::kSmem;
-    const unsigned grid = static_cast<unsigned>(2 * pairs);
-    if (i8) ragged_pair_kernel<true, false, NA><<<grid, kRgThreads, n, s>>>(w, b, p);
-    else if (a_mn) ragged_pair_kernel<false, true, NA><<<grid, kRgThreads, n, s>>>(w, b, p);
-    else ragged_pair_kernel<false, false, NA><<<grid, kRgThreads, n, s>>>(w, b, p);
+template <bool I8, bool A_MN, int NA>
+int launch_pair(int pairs, cudaStream_t s, const CUtensorMap &w, const RowMaps &b, const RaggedParams &p) {
+    ragged_pair_kernel<I8, A_MN, NA>
+        <<<static_cast<unsigned>(2 * pairs), kRgThreads, RpairCfg<NA>::kSmem, s>>>(w, b, p);
     return launch_status();
 }
 
@@ -195,7 +192,8 @@ struct RaggedPlan {
     int S, log_s;  // split kernels: CTAs per cluster
     int items;
 };
-RaggedPlan ragged_plan(const RaggedDevice &d, int E, int64_t R, int M, int n_kb, bool wide_ok) {
+// cut: rows that do not all start on 128-byte lines.
+RaggedPlan ragged_plan(const RaggedDevice &d, int E, int64_t R, int M, int n_kb, bool wide_ok, bool cut) {
     RaggedPlan P{};
     const int64_t groups = std::min<int64_t>(E, R);
     const int64_t mean = (R + groups - 1) / groups;
@@ -204,16 +202,23 @@ RaggedPlan ragged_plan(const RaggedDevice &d, int E, int64_t R, int M, int n_kb,
     P.few = mean <= 32;
     if (!P.few && pair_items >= d.pairs) {
         P.pair = 1;
-        // Two feature tiles per pair where the rounds come out shorter.  Cycles per k-step, one and two tiles: 690
-        // and 1060 where groups span several row tiles (bound by what L2 delivers), 760 and 1400 where the
-        // weights all come from HBM; two tiles add an epilogue that the products wait for.  Measured, one
-        // against two: 8 groups of 8192 rows 1.61 / 1.25 ms, 64 of 80 to 900 rows 0.60 / 0.52, 256 of 30 to
-        // 500 rows 1.38 / 1.27, 64 of 128 rows in INT8 172 / 181 us (fp32 results 172 / 188).
+        // Two feature tiles per pair where the rounds come out shorter.  Cycles per k-step of r rows: what L2
+        // delivers, 1.4 per 64 bytes staged, half as much again where rows do not start on 128-byte lines; or the
+        // products themselves, 2.75 r per 256 features under the power limit.  An item adds 2600 cycles, of two
+        // tiles 7400 (the products wait for its epilogue), and takes as long as its results take to write, 6100 and
+        // 15800; two tiles take a round more, for uneven last rounds.  Measured, one tile against two: 8 groups of
+        // 8192 rows, 5120 x 2560, 1174 / 1196 us; 32768 rows, 512 x 4096, 117 / 139; 56548 rows, 1000 x 1512
+        // (lines cut), 182 / 153; 64 groups of ~256 rows (often two tiles of ~133), input gradient of 5120 x 2560,
+        // 475 / 426; 256 of 128 rows, 5120 x 2560, 1345 / 1236; 16 of 256 rows, 2048 x 4096, 90 / 105.
         if (wide_ok) {
-            const bool one_tile = mean <= 192;
-            const int64_t wide_items = row_tiles * ((M + 2 * kPairRows - 1) / (2 * kPairRows));
-            const int64_t t1 = (pair_items + d.pairs - 1) / d.pairs * n_kb * (one_tile ? 760 : 690);
-            const int64_t t2 = (wide_items + d.pairs - 1) / d.pairs * (n_kb * int64_t(one_tile ? 1400 : 1060) + 2500);
+            const int64_t r = groups == 1 ? (mean + row_tiles - 1) / row_tiles : mean * kRpBN / (mean + kRpBN / 2);
+            const int64_t tiles = groups == 1 ? row_tiles : (groups * mean + r - 1) / r;
+            const int64_t rounds1 = (tiles * ((M + kPairRows - 1) / kPairRows) + d.pairs - 1) / d.pairs;
+            const int64_t rounds2 = (tiles * ((M + 2 * kPairRows - 1) / (2 * kPairRows)) + d.pairs - 1) / d.pairs + 1;
+            const int64_t step1 = std::max((256 + r) * (cut ? 9 : 6) * 11 / 48, r * 11 / 4);
+            const int64_t step2 = std::max((512 + r) * (cut ? 9 : 6) * 11 / 48, r * 11 / 2);
+            const int64_t t1 = rounds1 * std::max<int64_t>(n_kb * step1 + 2600, 6100);
+            const int64_t t2 = rounds2 * std::max<int64_t>(n_kb * step2 + 7400, 15800);
             if (t2 < t1) P.pair = 2;
         }
         return P;
@@ -274,7 +279,8 @@ int ragged_product(const RaggedCall &c, cudaStream_t s) {
     const int kelems = kRgRowBytes / esize;
     const int n_kb = (width + kelems - 1) / kelems;
     const RaggedPlan P = ragged_plan(d, c.E, c.R, M, n_kb,
-                                     c.i8 || (c.out_type != BEAM_MOE_F32 && one_segment_ok(c.dtype, width)));
+                                     !c.i8 && c.out_type != BEAM_MOE_F32 && one_segment_ok(c.dtype, width),
+                                     (c.ld_rows | c.K) * esize % 128 != 0);
     RaggedParams p{};
     p.offsets = c.offsets;
     p.out = c.out;
@@ -301,8 +307,12 @@ int ragged_product(const RaggedCall &c, cudaStream_t s) {
             if (!map_rows(&m_b.m[i], esize, c.rows, width, c.ld_rows, c.R, kbox,
                           static_cast<uint32_t>((i + 1) * kRpBoxStep)))
                 return BEAM_MOE_ERR_CUDA;
-        return P.pair == 1 ? launch_pair<1>(c.i8, c.dgrad, d.pairs, s, m_w, m_b, p)
-                           : launch_pair<2>(c.i8, c.dgrad, d.pairs, s, m_w, m_b, p);
+        if (c.i8) return launch_pair<true, false, 1>(d.pairs, s, m_w, m_b, p);
+        if (c.dgrad)
+            return P.pair == 1 ? launch_pair<false, true, 1>(d.pairs, s, m_w, m_b, p)
+                               : launch_pair<false, true, 2>(d.pairs, s, m_w, m_b, p);
+        return P.pair == 1 ? launch_pair<false, false, 1>(d.pairs, s, m_w, m_b, p)
+                           : launch_pair<false, false, 2>(d.pairs, s, m_w, m_b, p);
     }
     CUtensorMap m_b;
     if (!map_rows(&m_b, esize, c.rows, width, c.ld_rows, c.R, kbox,
