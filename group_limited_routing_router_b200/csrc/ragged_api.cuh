@@ -200,31 +200,11 @@ RaggedPlan ragged_plan(const RaggedDevice &d, int E, int64_t R, int M, int n_kb,
     const int64_t row_tiles = groups * ((mean + kRpBN - 1) / kRpBN);
     const int64_t pair_items = row_tiles * ((M + kPairRows - 1) / kPairRows);
     P.few = mean <= 32;
-    if (!P.few && pair_items >= d.pairs) {
-        P.pair = 1;
-        // Two feature tiles per pair where the rounds come out shorter.  Cycles per k-step of r rows: what L2
-        // delivers, 1.4 per 64 bytes staged, half as much again where rows do not start on 128-byte lines; or the
-        // products themselves, 2.75 r per 256 features under the power limit.  An item adds 2600 cycles, of two
-        // tiles 7400 (the products wait for its epilogue), and takes as long as its results take to write, 6100 and
-        // 15800; two tiles take a round more, for uneven last rounds.  Measured, one tile against two: 8 groups of
-        // 8192 rows, 5120 x 2560, 1174 / 1196 us; 32768 rows, 512 x 4096, 117 / 139; 56548 rows, 1000 x 1512
-        // (lines cut), 182 / 153; 64 groups of ~256 rows (often two tiles of ~133), input gradient of 5120 x 2560,
-        // 475 / 426; 256 of 128 rows, 5120 x 2560, 1345 / 1236; 16 of 256 rows, 2048 x 4096, 90 / 105.
-        if (wide_ok) {
-            const int64_t r = groups == 1 ? (mean + row_tiles - 1) / row_tiles : mean * kRpBN / (mean + kRpBN / 2);
-            const int64_t tiles = groups == 1 ? row_tiles : (groups * mean + r - 1) / r;
-            const int64_t rounds1 = (tiles * ((M + kPairRows - 1) / kPairRows) + d.pairs - 1) / d.pairs;
-            const int64_t rounds2 = (tiles * ((M + 2 * kPairRows - 1) / (2 * kPairRows)) + d.pairs - 1) / d.pairs + 1;
-            const int64_t step1 = std::max((256 + r) * (cut ? 9 : 6) * 11 / 48, r * 11 / 4);
-            const int64_t step2 = std::max((512 + r) * (cut ? 9 : 6) * 11 / 48, r * 11 / 2);
-            const int64_t t1 = rounds1 * std::max<int64_t>(n_kb * step1 + 2600, 6100);
-            const int64_t t2 = rounds2 * std::max<int64_t>(n_kb * step2 + 7400, 15800);
-            if (t2 < t1) P.pair = 2;
-        }
-        return P;
-    }
     const int bn = P.few ? 32 : 128;
-    const int64_t items = groups * ((mean + bn - 1) / bn) * ((M + kBM - 1) / kBM);
+    // groups around the mean have half a row tile more than it fills, on average (16 of ~256 rows: 48 tiles, not 32)
+    const int64_t halves =
+        groups == 1 || 4 * mean <= 3 * bn ? 2 * ((mean + bn - 1) / bn) : (2 * mean + bn - 1) / bn + 1;
+    const int64_t items = (groups * halves + 1) / 2 * ((M + kBM - 1) / kBM);
     int64_t best = 0;
     for (int i = 0; i < 4; ++i) {
         const int S = 1 << i;
@@ -241,6 +221,31 @@ RaggedPlan ragged_plan(const RaggedDevice &d, int E, int64_t R, int M, int n_kb,
         }
     }
     P.items = static_cast<int>(std::min<int64_t>(items, 1 << 30));
+    if (P.few) return P;
+    // Two feature tiles per pair where the rounds come out shorter.  Cycles per k-step of r rows: what L2
+    // delivers, 1.4 per 64 bytes staged, half as much again where rows do not start on 128-byte lines; or the
+    // products themselves, 2.75 r per 256 features under the power limit.  An item adds 2600 cycles, of two
+    // tiles 7400 (the products wait for its epilogue), and takes as long as its results take to write, 6100 and
+    // 15800; two tiles take half a round more, for uneven last rounds.  Measured, one tile against two: 8 groups of
+    // 8192 rows, 5120 x 2560, 1174 / 1196 us; 32768 rows, 512 x 4096, 117 / 139; 56548 rows, 1000 x 1512
+    // (lines cut), 182 / 153; 64 groups of ~256 rows (often two tiles of ~133), input gradient of 5120 x 2560,
+    // 475 / 426; 256 of 128 rows, 5120 x 2560, 1345 / 1236; 16 of 256 rows, 2048 x 4096, 90 / 105; 8 of 950 rows,
+    // 2728 x 4808 (cut), 213 / 188.
+    const int64_t r = groups == 1 ? (mean + row_tiles - 1) / row_tiles : mean * kRpBN / (mean + kRpBN / 2);
+    const int64_t tiles = groups == 1 ? row_tiles : (groups * mean + r - 1) / r;
+    const int64_t rounds1 = (tiles * ((M + kPairRows - 1) / kPairRows) + d.pairs - 1) / d.pairs;
+    const int64_t rounds2 = (tiles * ((M + 2 * kPairRows - 1) / (2 * kPairRows)) + d.pairs - 1) / d.pairs;
+    const int64_t line = cut ? 9 : 6;
+    const int64_t step1 = std::max((256 + r) * line * 11 / 48, r * 11 / 4);
+    const int64_t step2 = std::max((512 + r) * line * 11 / 48, r * 11 / 2);
+    const int64_t t1 = 2 * rounds1 * std::max<int64_t>(n_kb * step1 + 2600, 6100);
+    const int64_t t2 = (2 * rounds2 + 1) * std::max<int64_t>(n_kb * step2 + 7400, 15800);
+    // Fewer items than pairs go to the pairs where that is shorter by a tenth than splitting the contraction, by
+    // the same cycles per k-step (split against pairs: 9312 rows in 4 groups, 5144 x 240, 82 / 47 us; 4096 rows,
+    // 4096 x 1024, 53 / 35; 768 rows, 4096 x 4096, 51 / 33; 5000 rows in 32 groups, 2560 x 512, 45 / 31).
+    const int64_t split = 2 * best * (256 + 2 * std::min<int64_t>(mean, 128)) * line * 11 / 48;
+    if (pair_items < d.pairs && 10 * t1 > 9 * split) return P;
+    P.pair = wide_ok && t2 < t1 && pair_items >= d.pairs ? 2 : 1;
     return P;
 }
 
@@ -497,7 +502,8 @@ int beam_moe_grouped_mm_wgrad(int32_t n_experts, int64_t R, int32_t K, int32_t N
     else if (out_dtype == BEAM_MOE_F16)
         ragged_join_kernel<BEAM_MOE_F16><<<grid, 256, 0, s>>>(part, splits, n4, 0, dw, offsets, n_experts, R);
     else
-        ragged_join_kernel<BEAM_MOE_F32><<<grid, 256, 0, s>>>(part, splits, n4, accumulate != 0, dw, offsets, n_experts, R);
+        ragged_join_kernel<BEAM_MOE_F32>
+            <<<grid, 256, 0, s>>>(part, splits, n4, accumulate != 0, dw, offsets, n_experts, R);
     return launch_status();
 }
 
