@@ -124,6 +124,25 @@ def test_products_and_gradients(E, R, K, N, dtype):
         check_all(got, ref, N, K, counts, out_dtype, f"{out_dtype}")
 
 
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("E,R,K,N", [(1, 12000, 1032, 2056), (1, 12000, 2056, 1032), (32, 20000, 776, 1544),
+                                     (8, 20000, 1032, 2056), (4, 3000, 2568, 264), (1, 2100, 520, 2312)])
+def test_bands_of_row_tiles(E, R, K, N, dtype):
+    """Groups of many row tiles (whole and cut bands of them) over several feature tiles, two per pair among them;
+    few items on the pairs."""
+    g = gen(R + N)
+    counts = ragged_counts(E, R, N)
+    x, dy, w = normal(g, R, K, dtype=dtype), normal(g, R, N, dtype=dtype), normal(g, E, N, K, dtype=dtype,
+                                                                                scale=K ** -0.5)
+    off = offsets_of(counts)
+    ref = products(x, dy, w, counts)
+    got = dict(out=bm.grouped_mm(x, w, off), dx=bm.grouped_mm_dgrad(dy, w, off))
+    status_ok()
+    for name, length in (("out", K), ("dx", N)):
+        v, mag = ref[name]
+        check(got[name], v, half_step(v, dtype) + sum_tol(mag, length, dtype), name)
+
+
 @pytest.mark.parametrize("mean", [1, 12, 33, 64, 130, 400])
 def test_every_group_size(mean):
     """Groups of every size around the tiles' edges, empty ones among them."""
@@ -356,6 +375,24 @@ def test_int8_product(E, R, K, N, out_dtype):
     for e, a, b in spans(counts):
         want[a:b] = (q[a:b].to(D) @ w[e].to(D).t()) * rs[a:b].to(D)[:, None] * cs[e].to(D)
     check(out, want, half_step(want, out_dtype) + want.abs() * (3 * 2.0 ** -24 * 1.01), f"{out_dtype}")
+
+
+@pytest.mark.parametrize("out_dtype", [BF, HF, F32])
+@pytest.mark.parametrize("E,R,K,N", [(4, 3000, 2560, 272), (1, 12000, 144, 1040), (1, 2100, 528, 2320)])
+def test_int8_results_keep_to_their_columns(E, R, K, N, out_dtype):
+    """Results in a wider tensor's columns, rows in bands: what lies beside them stays."""
+    g = gen(R + K)
+    q, rs, w, cs = i8_operands(g, E, R, K, N)
+    rs = rs * (1.0 / K)
+    counts = ragged_counts(E, R, K)
+    wide = torch.full((R, N + 48), 3.0, dtype=out_dtype, device="cuda")
+    bm.grouped_mm_i8(q, rs, w, cs, offsets_of(counts), out=wide[:, 16:16 + N])
+    status_ok()
+    assert (wide[:, :16] == 3).all() and (wide[:, 16 + N:] == 3).all()
+    want = torch.zeros(R, N, dtype=D, device="cuda")
+    for e, a, b in spans(counts):
+        want[a:b] = (q[a:b].to(D) @ w[e].to(D).t()) * rs[a:b].to(D)[:, None] * cs[e].to(D)
+    check(wide[:, 16:16 + N], want, half_step(want, out_dtype) + want.abs() * (3 * 2.0 ** -24 * 1.01), f"{out_dtype}")
 
 
 def test_int8_largest_sums():
