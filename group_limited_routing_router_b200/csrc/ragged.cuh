@@ -27,6 +27,7 @@
 
 #include "gemm_2sm.cuh"
 #include "gemm_mx8.cuh"
+#include "launch.cuh"
 
 namespace beam {
 
@@ -495,6 +496,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kRgThreads, 1)
         fence_mbar_init();
         prefetch_tensormap(&tm_w);
     }
+    wait_for_stream();
     if (warp == 1) {
         tmem_alloc_pair(tmem_slot, 512);
         tmem_relinquish_pair();
@@ -811,6 +813,7 @@ __global__ void __launch_bounds__(kRgThreads, 1)
         prefetch_tensormap(&tm_w);
         prefetch_tensormap(&tm_b);
     }
+    wait_for_stream();
     if (warp == 1) {
         tmem_alloc(tmem_slot, 2 * C::kSlot);
         tmem_relinquish();
@@ -1230,6 +1233,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kRwThreads, 1)
         prefetch_tensormap(&tm_x);
         prefetch_tensormap(&tm_dw);
     }
+    wait_for_stream();
     if (warp == 1) {
         tmem_alloc_pair(tmem_slot, 512);
         tmem_relinquish_pair();

@@ -10,6 +10,7 @@
 #include <cuda_fp16.h>
 
 #include "common.cuh"
+#include "launch.cuh"
 
 namespace beam {
 
@@ -109,6 +110,8 @@ struct SwigluParams {
 // Threads (x, y): eight columns each, rows y, y + gridDim.y blockDim.y, ...
 template <typename T, bool BACKWARD>
 __global__ void __launch_bounds__(256) swiglu_kernel(const SwigluParams p) {
+    let_next_launch();
+    wait_for_stream();
     const int c = (blockIdx.x * blockDim.x + threadIdx.x) * 8;
     if (c >= p.I) return;
     const T *gp = reinterpret_cast<const T *>(p.g), *up = reinterpret_cast<const T *>(p.u);
@@ -241,6 +244,8 @@ constexpr int kQuantCached = 4;
 // Values past the cached steps are read again.
 template <typename T, bool SWIGLU, bool WARP_ROW>
 __global__ void __launch_bounds__(512) quant_i8_kernel(const QuantParams p) {
+    let_next_launch();
+    wait_for_stream();
     constexpr int kSteps = kQuantCached;
     __shared__ uint32_t part[16];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;

@@ -638,6 +638,49 @@ def test_captured_and_replayed_with_other_groups():
     status_ok()
 
 
+@pytest.mark.parametrize("R,E", [(1, 1), (40, 8), (700, 8), (9000, 2)])
+def test_calls_that_follow_one_another(R, E):
+    """Calls back to back over the same buffers, with other work of the stream between them, eager and captured: each
+    sees what the one before it wrote, and nothing is written before its last reader is done."""
+    I, H, n = 320, 512, 12
+    g = gen(R)
+    off = offsets_of(ragged_counts(E, R, 4, empty=0.0))
+    q8, _, w8, cs = i8_operands(g, E, R, H, I)
+    w, down = normal(g, E, I, H, scale=H ** -0.5), normal(g, E, H, I, scale=I ** -0.5)
+    x, steps = torch.empty(R, H, dtype=BF, device="cuda"), normal(g, n, R, H)
+    q, s = torch.empty_like(q8), torch.empty(R, device="cuda")
+    a, b, h = (torch.empty(R, I, dtype=BF, device="cuda") for _ in range(3))
+    dx, dw = torch.empty_like(x), torch.zeros(E, H, I, device="cuda")
+    out = torch.empty(n, 2, R, H, dtype=BF, device="cuda")
+
+    def run(sync):
+        dw.zero_()
+        for i in range(n):
+            calls = (lambda: x.copy_(steps[i]), lambda: bm.quant_i8_rows(x, q, s),
+                     lambda: bm.grouped_mm_i8(q, s, w8, cs, off, out=a), lambda: bm.grouped_mm(x, w, off, out=b),
+                     lambda: bm.swiglu(b, b, out=h), lambda: bm.grouped_mm(h, down, off, out=out[i, 0]),
+                     lambda: bm.swiglu_backward(a, b, h, dg=a, du=b), lambda: bm.grouped_mm_dgrad(a, w, off, out=dx),
+                     lambda: bm.grouped_mm_wgrad(dx, b, off, out=dw, accumulate=True), lambda: out[i, 1].copy_(dx))
+            for f in calls:
+                f()
+                if sync:
+                    torch.cuda.synchronize()
+        return out.clone(), dw.clone()
+
+    want = run(True)
+    got = [run(False) for _ in range(3)]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        captured = run(False)
+    for _ in range(2):
+        graph.replay()
+        torch.cuda.synchronize()
+        got.append(tuple(t.clone() for t in captured))
+    status_ok()
+    for result in got:
+        assert all(torch.equal(r.nan_to_num(), v.nan_to_num()) for r, v in zip(result, want))
+
+
 def test_two_calls_at_once():
     """Products of different kernels on two streams, overlapping: each gives what it gives alone."""
     g = gen(61)
