@@ -283,7 +283,11 @@ __device__ __forceinline__ void pack_chunk(int sub, float rs, const float (&ch)[
 }
 // Stores a packed chunk of 16 rows from row c on.  q: this warp's 32 of the 128 features from mt0 on (M is a
 // multiple of 8); stage: its four warps' two buffers, between which `flip` alternates, so that one barrier per
-// chunk orders a buffer's writes after the reads of two chunks ago.  live: false after a wait has timed out.
+// chunk orders a buffer's writes after the reads of two chunks ago.  live: false after a wait has timed out.  TIGHT:
+// a row's 16 bytes at a time, where two tiles' packed sums leave few registers (NA = 2, 64 groups of ~256 rows, input
+// gradient of 5120 x 2560: 415 -> 407 us); both rows together where the stores are the bound (NA = 1, 45231 rows,
+// 224 x 4328: 5 to 15% less).
+template <bool TIGHT>
 __device__ __forceinline__ void store_chunk(const RaggedParams &p, const RaggedItem &it, int c, int mt0, int q, int sub,
                                             uint32_t stage, int flip, bool live, const uint32_t (&pk)[8]) {
     const int lane = threadIdx.x & 31;
@@ -295,13 +299,26 @@ __device__ __forceinline__ void store_chunk(const RaggedParams &p, const RaggedI
         stmatrix_trans(at + 8 * 256, {pk[4], pk[5], pk[6], pk[7]});
     }
     quad_sync(sub);
-    const int row = 4 * q + (lane >> 4), piece = lane & 15;  // rows 4 q, 4 q + 1, then the next two
-    const uint32_t at = buf + row * 256;
-    const uint4 lo = lds128(at + ((piece ^ (row & 7)) << 4)), hi = lds128(at + 512 + ((piece ^ ((row + 2) & 7)) << 4));
-    if (live && mt0 + 8 * piece < p.M) {
-        uint16_t *o = reinterpret_cast<uint16_t *>(p.out) + (it.row0 + c + row) * p.ldo + mt0 + 8 * piece;
-        if (c + row < it.n_valid) *reinterpret_cast<uint4 *>(o) = lo;
-        if (c + row + 2 < it.n_valid) *reinterpret_cast<uint4 *>(o + 2 * p.ldo) = hi;
+    // rows 4 q and 4 q + 1, then the next two
+    const int piece = lane & 15;
+    if constexpr (TIGHT) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int row = 4 * q + 2 * i + (lane >> 4), m = mt0 + 8 * piece;
+            const uint4 v = lds128(buf + row * 256 + ((piece ^ (row & 7)) << 4));
+            if (live && c + row < it.n_valid && m < p.M)
+                *reinterpret_cast<uint4 *>(reinterpret_cast<uint16_t *>(p.out) + (it.row0 + c + row) * p.ldo + m) = v;
+        }
+    } else {
+        const int row = 4 * q + (lane >> 4);
+        const uint32_t at = buf + row * 256;
+        const uint4 lo = lds128(at + ((piece ^ (row & 7)) << 4));
+        const uint4 hi = lds128(at + 512 + ((piece ^ ((row + 2) & 7)) << 4));
+        if (live && mt0 + 8 * piece < p.M) {
+            uint16_t *o = reinterpret_cast<uint16_t *>(p.out) + (it.row0 + c + row) * p.ldo + mt0 + 8 * piece;
+            if (c + row < it.n_valid) *reinterpret_cast<uint4 *>(o) = lo;
+            if (c + row + 2 < it.n_valid) *reinterpret_cast<uint4 *>(o + 2 * p.ldo) = hi;
+        }
     }
 }
 
@@ -400,7 +417,7 @@ __device__ __forceinline__ void store_item(const RaggedParams &p, const RaggedIt
             if (c < it.n_valid) {  // the same for the four warps
                 uint32_t pk[8];
                 pack_chunk<I8, TYPE>(sub, rs[i], ch, acc[i], pk);
-                store_chunk(p, it, c, mt0, q, sub, stage, i, live, pk);
+                store_chunk<false>(p, it, c, mt0, q, sub, stage, i, live, pk);
             }
         }
         quad_sync(sub);  // the next item starts with the first buffer again
@@ -454,7 +471,7 @@ __device__ __forceinline__ void store_packed(const RaggedParams &p, const Ragged
 #pragma unroll
         for (int i = 0; i < kRpBN / 32; ++i)
             if (16 * sub + 32 * i < it.n_valid)  // the same for the four warps
-                store_chunk(p, it, 16 * sub + 32 * i, mt0 + a * kPairRows, q, sub, stage, i, live, pk[a][i]);
+                store_chunk<NA == 2>(p, it, 16 * sub + 32 * i, mt0 + a * kPairRows, q, sub, stage, i, live, pk[a][i]);
         quad_sync(sub);  // the buffers' turns start over
     }
 }
