@@ -84,14 +84,15 @@ __device__ __forceinline__ float exp2_fast(float x) {
 // sigma(g) = 1 / (1 + e^-g).  16-bit data: the fast exponential and quotient, whose error (|g| 2^-24 from the
 // rounded product with log2 e) is far below the result's rounding.  fp32 data: that product's rounding error is
 // kept and applied to first order, e^x = 2^p (1 + r ln 2) with p + r = x log2 e, which leaves a few 2^-23; the
-// argument is clamped where e^x is 0 or +inf anyway, so that r stays small.
+// argument is clamped so that r stays small and e^x finite (an infinite one plus a negative correction would be NaN).
+// Both give 0 for a sigma below 2^-126, g < -87.34: the quotient is 0 for a divisor above 2^126, which e^88 is.
 template <typename T>
 __device__ __forceinline__ float sigmoid_of(float g) {
     if constexpr (sizeof(T) == 2) {
         return __fdividef(1.0f, 1.0f + __expf(-g));
     } else {
         constexpr float kLog2e = 1.44269504f, kLog2eLow = 1.92596299e-8f, kLn2 = 0.693147181f;
-        const float x = g != g ? g : fminf(fmaxf(-g, -126.0f), 126.0f);
+        const float x = g != g ? g : fminf(fmaxf(-g, -126.0f), 88.0f);
         const float p = x * kLog2e;
         const float r = fmaf(x, kLog2eLow, fmaf(x, kLog2e, -p));
         const float e = exp2_fast(p);

@@ -533,6 +533,56 @@ def test_swiglu_int8(R, I, dtype):
     assert ((q.to(D) - h / scale[:, None]).abs() <= 0.5 + 127 * 2.0 ** -17).all()
 
 
+def gates(R, I, dtype, across):
+    """[R, I] gates: every 2^-8 from -130 to 130 and the type's largest of both signs; neighbours in a row, or
+    (across) in a column, so that each row spans them all."""
+    g = torch.arange(R * I, dtype=D, device="cuda") / 256 - 130
+    g[-1], g[0] = torch.finfo(dtype).max, torch.finfo(dtype).min
+    return (g.view(I, R).t() if across else g.view(R, I)).contiguous().to(dtype)
+
+
+@pytest.mark.parametrize("across", [False, True])
+@pytest.mark.parametrize("dtype", [BF, HF, F32])
+@pytest.mark.parametrize("R,I", [(260, 256), (13, 5120)])
+def test_swiglu_of_every_gate(R, I, dtype, across):
+    """Gates over the whole range of the exponential and past it: results are finite and the formula's.  A sigma
+    below 2^-126 may be 0, so results are off by (1 + |g|) 2^-126 more (|u|, |dh| <= 1), and products of few
+    2^-149 round to the subnormals."""
+    rng = gen(I)
+    g = gates(R, I, dtype, across)
+    u, dh = ((torch.rand(R, I, generator=rng, device="cuda") * 2 - 1).to(dtype) for _ in range(2))
+    h, dg, du = bm.swiglu(g, u), *bm.swiglu_backward(dh, g, u)
+    status_ok()
+    wh, wg, wu = swiglu_ref(dh, g, u)
+    gd, ud, dd = g.to(D), u.to(D), dh.to(D)
+    rel = (24 + 2 * gd.abs().clamp_max(130)) * 2.0 ** -24
+    low = (1 + gd.abs().clamp_max(130)) * 2.0 ** -126 + 2.0 ** -146
+    for t in (h, dg, du):
+        assert t.isfinite().all()
+    check(h, wh, half_step(wh, dtype) + wh.abs() * rel + low, "h")
+    check(du, wu, half_step(wu, dtype) + wu.abs() * rel + low, "du")
+    check(dg, wg, half_step(wg, dtype) + (dd * ud).abs() * torch.sigmoid(gd) * (1 + gd.abs()) * rel + low, "dg")
+
+
+@pytest.mark.parametrize("across", [False, True])
+@pytest.mark.parametrize("dtype", [BF, HF, F32])
+@pytest.mark.parametrize("R,I", [(260, 256), (13, 5120), (3, 22528)])
+def test_swiglu_int8_of_every_gate(R, I, dtype, across):
+    """The same gates through the quantiser: h within (24 + 2 x 130) 2^-24, the scale within that and three
+    roundings more, so a code is within half a step and 127 times both; rows of vanishing h alone have scale 0."""
+    rng = gen(I + 1)
+    g = gates(R, I, dtype, across)
+    u = (torch.rand(R, I, generator=rng, device="cuda") * 2 - 1).to(dtype)
+    q, s = bm.swiglu_i8(g, u)
+    status_ok()
+    h = swiglu_ref(torch.zeros_like(g), g, u)[0]
+    low, rel = 131 * 2.0 ** -126, 284 * 2.0 ** -24
+    assert s.isfinite().all()
+    check(s, h.abs().amax(dim=1) / 127, h.abs().amax(dim=1) / 127 * (rel + 3 * 2.0 ** -24) + low, "scale")
+    step = s.to(D)[:, None]
+    check(q.to(D) * step, h, step * (0.5 + 127 * (2 * rel + 4 * 2.0 ** -24)) + low, "codes")
+
+
 # ---- together ---------------------------------------------------------------------------------------
 def test_layer_training_step():
     """Router, dispatch, both first products, SwiGLU, second product and combine, then the experts'
