@@ -5,8 +5,9 @@
 namespace beam {
 
 // First of all that touches global memory or TMEM, by every thread: returns when the stream's last kernel has
-// completed and its writes are visible.  What was read behind it must not be a non-coherent load that the compiler
-// could move ahead of it.  A kernel that returns before it would let the next one overtake that kernel.
+// completed and its writes are visible.  Nothing is read by non-coherent loads (ld.global.nc, __ldg, pointers to const
+// __restrict__): they are for data that nobody writes while the kernel lives, which here includes the end of the one
+// before.  A kernel that returns before the wait would let the next one overtake that kernel.
 __device__ __forceinline__ void wait_for_stream() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 // The next kernel may be launched once every block has come here.  For short kernels of small blocks: the next one's

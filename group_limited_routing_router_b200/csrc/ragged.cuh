@@ -250,7 +250,7 @@ __device__ __forceinline__ void channel_scales(const RaggedParams &p, int e, int
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const int m = m0 + ((threadIdx.x & 31) >> 2) + 8 * i;
-        ch[i] = (I8 && m < p.M) ? __ldg(p.channel_scale + static_cast<int64_t>(e) * p.M + m) : 1.0f;
+        ch[i] = (I8 && m < p.M) ? p.channel_scale[static_cast<int64_t>(e) * p.M + m] : 1.0f;
     }
 }
 // Scales of the item's rows, 32 i + lane, asked for before its sums are waited for: they would cost every chunk
@@ -260,7 +260,7 @@ __device__ __forceinline__ void row_scales(const RaggedParams &p, const RaggedIt
 #pragma unroll
     for (int i = 0; i < CHUNKS; ++i) {
         const int row = 32 * i + (threadIdx.x & 31);
-        rs[i] = (I8 && row < it.n_valid) ? __ldg(p.row_scale + it.row0 + row) : 1.0f;
+        rs[i] = (I8 && row < it.n_valid) ? p.row_scale[it.row0 + row] : 1.0f;
     }
 }
 // A chunk of 16 rows: the 16 words of its two fragment loads to 8 words of packed pairs, for the two halves of 8
@@ -395,7 +395,7 @@ __device__ __forceinline__ void store_item(const RaggedParams &p, const RaggedIt
                                            const uint32_t (&acc)[CHUNKS][16]) {
     if constexpr (TYPE == BEAM_MOE_F32) {
         const int m = mt0 + 32 * q + (threadIdx.x & 31);
-        const float channel = (I8 && m < p.M) ? __ldg(p.channel_scale + static_cast<int64_t>(it.e) * p.M + m) : 1.0f;
+        const float channel = (I8 && m < p.M) ? p.channel_scale[static_cast<int64_t>(it.e) * p.M + m] : 1.0f;
 #pragma unroll
         for (int i = 0; i < CHUNKS; ++i) {
             const int c = 16 * sub + 32 * i;
@@ -447,7 +447,7 @@ __device__ __forceinline__ void pack_item(const RaggedItem &it, uint32_t t, int 
 __device__ __forceinline__ void store_i8_f32(const RaggedParams &p, const RaggedItem &it, uint32_t t, int sub, int m0,
                                              bool live, const float (&rs)[kRpBN / 32]) {
     const int m = m0 + (threadIdx.x & 31);
-    const float channel = m < p.M ? __ldg(p.channel_scale + static_cast<int64_t>(it.e) * p.M + m) : 1.0f;
+    const float channel = m < p.M ? p.channel_scale[static_cast<int64_t>(it.e) * p.M + m] : 1.0f;
 #pragma unroll
     for (int i = 0; i < kRpBN / 32; ++i) {
         const int c = 16 * sub + 32 * i;
@@ -741,7 +741,7 @@ __device__ __forceinline__ void reduce_store(const RaggedParams &p, const Ragged
     const int log_f = 31 - __clz(F);
     const int total = ((it.n_valid + 3) >> 2) << log_f;  // four-row pieces
     const int f = tid & (F - 1), m = m0 + f;             // F divides 256: a thread keeps its feature
-    const float channel = (I8 && m < p.M) ? __ldg(p.channel_scale + static_cast<int64_t>(it.e) * p.M + m) : 1.0f;
+    const float channel = (I8 && m < p.M) ? p.channel_scale[static_cast<int64_t>(it.e) * p.M + m] : 1.0f;
     for (int idx = tid; idx - (tid & 31) < total; idx += 32 * kGemmEpiWarps) {  // warp-uniform
         const int quad = idx >> log_f;
         const bool live = idx < total && m < p.M;
@@ -763,7 +763,7 @@ __device__ __forceinline__ void reduce_store(const RaggedParams &p, const Ragged
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const int c = 4 * quad + j;
-                const float row = (I8 && c < it.n_valid) ? __ldg(p.row_scale + it.row0 + c) : 1.0f;
+                const float row = (I8 && c < it.n_valid) ? p.row_scale[it.row0 + c] : 1.0f;
                 v[j] = ragged_value<I8>(w[j], channel, row);
             }
         }

@@ -501,7 +501,8 @@ BEAM_MOE_API int beam_moe_grouped_mm_i8(int32_t n_experts, int64_t R, int32_t K,
 
 /*
  * SwiGLU between the products: h = SiLU(g) * u, elementwise over [R, I] in dtype (any; FP32 arithmetic, in
- * which a sigmoid below 2^-126, for g < -87.34, is 0; the same in the calls below).  h may be g's or u's own buffer (with the same stride).
+ * which a sigmoid below 2^-126, for g < -87.34, is 0; the same in the calls below).  h may be g's or u's own
+ * buffer (with the same stride).
  */
 BEAM_MOE_API int beam_moe_swiglu(int64_t R, int32_t I, int dtype, const void *g, int64_t ldg, const void *u,
                                  int64_t ldu, void *h, int64_t ldh, void *stream);

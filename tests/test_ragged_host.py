@@ -1,6 +1,7 @@
 """Refusals of the grouped products, the INT8 products and SwiGLU: the C ABI's codes on the host, before
 any CUDA call (the pointers are never dereferenced), and the binding's checks on CPU tensors."""
 import ctypes
+import os
 
 import pytest
 import torch
@@ -152,3 +153,16 @@ def test_binding_refuses_cpu_tensors(L):
               lambda: bm.grouped_mm_i8(None, None, None, None)):
         with pytest.raises(TypeError):
             f()
+
+
+def test_no_load_is_non_coherent():
+    """Kernels that are launched while the stream's last one still runs live while it writes what they read (the
+    quantiser's row scales): non-coherent loads are not for such data.  The join kernel is launched after it."""
+    csrc = os.path.join(os.path.dirname(bm.__file__), "csrc")
+    for name in ("ragged.cuh", "swiglu.cuh"):
+        with open(os.path.join(csrc, name)) as f:
+            code = f.read()
+        assert "launch_after(ragged_join" not in code and "wait_for_stream();" in code
+        kernels = code.split("void __launch_bounds__(256) ragged_join_kernel")[0]
+        for load in ("__ldg", "ld.global.nc", "__restrict__", "__ldlu", "__ldcv"):
+            assert load not in kernels, (name, load)
