@@ -102,11 +102,25 @@ __device__ __forceinline__ uint32_t idesc_with_n(uint32_t idesc, int n) {
     return idesc | (static_cast<uint32_t>(n >> 3) << 17);
 }
 
-// Arrives on a barrier of any CTA of the cluster.  What is handed over is TMEM, ordered by the tcgen05 fences on
-// both sides, or shared memory, after a proxy fence or to be overwritten: no other memory operation has to be
-// performed first, which a release at cluster scope would wait for.
+// Arrives on a barrier of any CTA of the cluster without a release at cluster scope, which would wait for all of the
+// thread's earlier memory operations.  What is handed over is TMEM, ordered by the tcgen05 fences on both sides, or
+// shared memory that has been read (the values were used) and may be overwritten.
 __device__ __forceinline__ void mbar_arrive_async(uint32_t bar_cluster) {
     asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar_cluster) : "memory");
+}
+
+// The same behind a release at cluster scope of shared memory alone: what the warp has written there (and fenced for
+// the async proxy) is seen by whoever acquires it.  wgrad, 256 groups of ~78 rows, 512 x 512: 38 us as without any
+// release, 49 with one of all memory (64 groups of 128 rows, 5120 x 2560: 389 against 431).
+__device__ __forceinline__ void mbar_release_smem(uint32_t bar_cluster) {
+    asm volatile(
+        "fence.release.sync_restrict::shared::cta.cluster;\n\t"
+        "mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar_cluster)
+        : "memory");
+}
+// Its other side, behind the wait on the barrier (which acquires at CTA scope).
+__device__ __forceinline__ void acquire_smem() {
+    asm volatile("fence.acquire.sync_restrict::shared::cluster.cluster;" ::: "memory");
 }
 
 // ---- groups --------------------------------------------------------------------------------------
@@ -1018,7 +1032,8 @@ __global__ void __launch_bounds__(kRgThreads, 1)
 //            arrivals being the leader's producer's; for a k-step to clear the two helpers arrive on it
 //   tail[s]  this CTA's loads of a k-step to clear have landed
 // No producer arrives on the other CTA's barrier: one such release at cluster scope per k-step, which waits
-// for the thread's earlier memory operations, held the ring at 700 TFLOP/s (with or without the products).
+// for the thread's earlier memory operations, held the ring at 700 TFLOP/s (with or without the products).  The helper
+// of the peer does, with a release of shared memory alone.
 //
 // The epilogue stages 32 rows x 128 bytes per warp at a time, swizzled, and stores them with TMA, which clips
 // at N and K and, for `accumulate`, adds (FP32).  Groups without rows store zeros.
@@ -1360,6 +1375,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kRwThreads, 1)
                         }
                         tc_fence_after();
                         const uint32_t sa = smem_u32(smem + stage * C::kStage);
+                        if (needs_clearing(it.rows - kb * 64)) acquire_smem();
                         const uint64_t da = umma_desc_mn_sw128(sa);
                         const int n_mma16 = min(4, (it.rows - kb * 64 + 15) / 16);
                         for (int kk = 0; kk < n_mma16; ++kk)
@@ -1407,7 +1423,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kRwThreads, 1)
             }
             fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0) mbar_arrive_async(full_lead + 8u * stage);
+            if (lane == 0) {
+                if (rank == 0) mbar_arrive(&full[stage]);
+                else mbar_release_smem(full_lead + 8u * stage);
+            }
         }
     } else if (warp >= 4) {
         // ---------------- epilogue: lanes = rows n, two warps per quadrant share a product's columns

@@ -268,6 +268,29 @@ def test_weight_gradient_of_long_groups(counts, dtype):
     status_ok()
 
 
+@pytest.mark.parametrize("N,K", [(256, 1280), (520, 264)])
+def test_cleared_rows_of_many_short_groups(N, K):
+    """Every length of a last k-step, on both CTAs of a pair, with NaN in every other group: a sum that met a row
+    before it was cleared would be NaN."""
+    counts = [1 + (i * 37) % 190 for i in range(256)]
+    R = sum(counts)
+    g = gen(K)
+    dy, x = normal(g, R, N), normal(g, R, K)
+    v, mag = products(x, dy, torch.zeros(256, N, K, device="cuda"), counts)["dw"]
+    for e, a, b in spans(counts):
+        if e % 2:
+            dy[a:b] = float("nan")
+            x[a:b] = float("nan")
+    off = offsets_of(counts)
+    first = None
+    for _ in range(10):
+        dw = bm.grouped_mm_wgrad(dy, x, off)
+        check(dw[::2], v[::2], half_step(v[::2], BF) + sum_tol(mag[::2], max(counts), BF), "dw")
+        first = dw if first is None else first
+        assert torch.equal(dw[::2], first[::2]) and dw[1::2].isnan().all()
+    status_ok()
+
+
 def test_gradients_against_differences():
     """out is linear in x and in w: the change of sum(dy * out) along any direction is its gradient times
     that direction, exactly but for the roundings (fp32 results)."""

@@ -166,3 +166,14 @@ def test_no_load_is_non_coherent():
         kernels = code.split("void __launch_bounds__(256) ragged_join_kernel")[0]
         for load in ("__ldg", "ld.global.nc", "__restrict__", "__ldlu", "__ldcv"):
             assert load not in kernels, (name, load)
+
+
+def test_cleared_rows_are_released_to_the_cluster():
+    """The weight gradient's helper writes shared memory that the other CTA's products read: a release at cluster
+    scope on its side, an acquire on theirs."""
+    with open(os.path.join(os.path.dirname(bm.__file__), "csrc", "ragged.cuh")) as f:
+        code = f.read()
+    helper = code.split("helper: clears the rows behind the group")[1].split("epilogue: lanes = rows n")[0]
+    assert "mbar_release_smem(full_lead" in helper and "mbar_arrive_async" not in helper
+    issuer = code.split("ragged_wgrad_kernel(")[1].split("MMA issuer for the pair")[1].split("helper: clears")[0]
+    assert "if (needs_clearing(it.rows - kb * 64)) acquire_smem();" in issuer
