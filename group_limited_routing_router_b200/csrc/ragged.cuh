@@ -103,14 +103,13 @@ __device__ __forceinline__ uint32_t idesc_with_n(uint32_t idesc, int n) {
 }
 
 // Arrives on a barrier of any CTA of the cluster without a release at cluster scope, which would wait for all of the
-// thread's earlier memory operations.  What is handed over is TMEM, ordered by the tcgen05 fences on both sides, or
-// shared memory that has been read (the values were used) and may be overwritten.
+// thread's earlier memory operations.  What is handed over is TMEM, ordered by the tcgen05 fences on both sides.
 __device__ __forceinline__ void mbar_arrive_async(uint32_t bar_cluster) {
     asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar_cluster) : "memory");
 }
 
-// The same behind a release at cluster scope of shared memory alone: what the warp has written there (and fenced for
-// the async proxy) is seen by whoever acquires it.  wgrad, 256 groups of ~78 rows, 512 x 512: 38 us as without any
+// The same behind a release at cluster scope of shared memory alone: what the warp has read there may be overwritten
+// by whoever acquires it, and what it has written (and fenced for the async proxy) is seen.  wgrad, 256 groups of ~78 rows, 512 x 512: 38 us as without any
 // release, 49 with one of all memory (64 groups of 128 rows, 5120 x 2560: 389 against 431).
 __device__ __forceinline__ void mbar_release_smem(uint32_t bar_cluster) {
     asm volatile(
@@ -990,6 +989,7 @@ __global__ void __launch_bounds__(kRgThreads, 1)
             // the last item's partial sums have been read everywhere, then these are pushed
             ok = mbar_wait(red_empty, (n_item & 1u) ^ 1u, p.timeout);
             if (!ok) break;
+            acquire_smem();
 #pragma unroll
             for (int i = 0; i < kChunks; ++i) {
                 const int c = 16 * sub + 32 * i;
@@ -1001,6 +1001,7 @@ __global__ void __launch_bounds__(kRgThreads, 1)
             }
             ok = mbar_wait(red_full, n_item & 1u, p.timeout);
             if (!ok) break;
+            acquire_smem();
             const int tid = static_cast<int>(threadIdx.x) - 64;
             const int m0 = it.mt * kBM + static_cast<int>(rank) * F;
             if (p.out_type == BEAM_MOE_BF16) reduce_store<I8, BN, BEAM_MOE_BF16>(p, it, buf, S, F, m0, tid);
@@ -1008,7 +1009,7 @@ __global__ void __launch_bounds__(kRgThreads, 1)
             else reduce_store<I8, BN, BEAM_MOE_F32>(p, it, buf, S, F, m0, tid);
             __syncwarp();  // this warp has read its sums: one arrival per CTA of the cluster
             if (item + n_clusters < total && lane < static_cast<int>(S))
-                mbar_arrive_async(mapa_shared(smem_u32(red_empty), lane));
+                mbar_release_smem(mapa_shared(smem_u32(red_empty), lane));
         }
         if (!joined) cluster_wait();
     }

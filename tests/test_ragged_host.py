@@ -177,3 +177,15 @@ def test_cleared_rows_are_released_to_the_cluster():
     assert "mbar_release_smem(full_lead" in helper and "mbar_arrive_async" not in helper
     issuer = code.split("ragged_wgrad_kernel(")[1].split("MMA issuer for the pair")[1].split("helper: clears")[0]
     assert "if (needs_clearing(it.rows - kb * 64)) acquire_smem();" in issuer
+
+
+def test_partial_sums_are_released_to_the_cluster():
+    """The split kernel's CTAs write their partial sums into one another's shared memory: where the last item's were
+    read, and where the new ones have arrived, the order holds at cluster scope on both sides."""
+    with open(os.path.join(os.path.dirname(bm.__file__), "csrc", "ragged.cuh")) as f:
+        code = f.read()
+    split = code.split("ragged_split_kernel(const")[1].split("// ---- wgrad on CTA pairs")[0]
+    for bar in ("red_empty, (n_item", "red_full, n_item"):
+        behind = split.split("mbar_wait(" + bar)[1].split(";")[1:3]
+        assert [s.strip() for s in behind] == ["if (!ok) break", "acquire_smem()"], bar
+    assert "mbar_release_smem(mapa_shared(smem_u32(red_empty), lane))" in split and "mbar_arrive_async" not in split
