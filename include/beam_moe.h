@@ -435,8 +435,15 @@ BEAM_MOE_API int beam_moe_permute_noalloc(const beam_moe_config *cfg, int64_t T,
  * over ragged rows ("each of the 8 selected experts is a SwiGLU MLP": "Welcome Beam" page, section
  * "Mixture of Experts"), the same products in INT8, and SwiGLU.  They take the dispatch order of
  * beam_moe_permute (its offsets, rows gathered by beam_moe_gather_rows).  Common to all of them:
- *   - Types are given as BEAM_MOE_BF16, BEAM_MOE_F16 or BEAM_MOE_F32.  Sums are FP32 (INT32 for INT8
- *     operands, exact) and rounded once, to nearest even, when stored.
+ *   - Types are given as BEAM_MOE_BF16, BEAM_MOE_F16 or BEAM_MOE_F32.  Results are rounded to nearest even
+ *     when stored.  INT8 sums are exact in INT32; the sum's conversion to FP32 and its two scales are a
+ *     rounding each.  Other sums are FP32, 16 products at a time: the tensor core truncates the running
+ *     sum after each 16, which takes up to 2^-25 per 16 off the end value of a sum that grows evenly, and far
+ *     less off one of mixed signs.  They are cut into pieces that are added to nearest:
+ *       fp32 results: pieces of 256 products (2^-21); in the weight gradient of long groups, pieces of 4096
+ *       rows where its 512-column tiles run (2^-17);
+ *       16-bit results: pieces of 1024 products (2^-19), or one piece on the 512-wide tiles where that takes off
+ *       at most an eighth of half a step of the result (up to 131072 products for bf16, 16384 for fp16).
  *   - R is the number of rows, 0..2^24.  Widths (K, N, I) are multiples of 8 (INT8 products: 16) in
  *     8..65536.  Matrices over rows have a row stride ld in elements (at least the width, at most 2^32;
  *     rows start on 16-byte boundaries); weights and weight gradients are densely packed.
@@ -468,7 +475,8 @@ BEAM_MOE_API int beam_moe_grouped_mm_dgrad(int32_t n_experts, int64_t R, int32_t
 /*
  * Gradient of beam_moe_grouped_mm in its weights: dw[e, n, k] = sum over the rows r of group e of
  * dy[r, n] x[r, k]; zero for a group without rows.  With `accumulate` (out_dtype F32 only) the sums are
- * added to dw instead; a group without rows then leaves its dw as it is.
+ * added to dw instead; a group without rows then leaves its dw as it is.  (Subnormal numbers in dw that are
+ * added to, or come of the addition, may be taken as 0.)  With R = 0 the offsets are not looked at.
  *   dy [R, N], x [R, K] in dtype; dw [n_experts, N, K] in out_dtype (dtype or F32)
  *   ws: beam_moe_grouped_mm_wgrad_workspace_size bytes, 16-byte aligned; that size is 0, and ws may be
  *   NULL, unless few weights meet many rows (the rows are then split and the partial sums added in order).

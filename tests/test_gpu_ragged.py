@@ -291,6 +291,73 @@ def test_cleared_rows_of_many_short_groups(N, K):
     status_ok()
 
 
+def one_signed(g, *shape, dtype=BF):
+    """Values in [1/2, 1]: sums of their products grow evenly, where truncation takes off the most."""
+    return (torch.rand(*shape, generator=g, device="cuda") / 2 + 0.5).to(dtype)
+
+
+def even_tol(want, piece, length):
+    """Error of an evenly growing sum of `length` products in pieces of `piece`: an instruction truncates less than
+    2^-22 of its running sum, half the piece's on average (a quarter more for its uneven growth); the pieces, and
+    up to 64 partial sums of split contractions, are added in FP32."""
+    m = min(piece, length) // 16 + 1
+    return want * ((m / 2 + 1) * 1.25 * 2.0 ** -22 + (length // piece + 66) * 2.0 ** -24)
+
+
+@pytest.mark.parametrize("E,R,K,N", [
+    (1, 3000, 20480, 1024),  # CTA pairs
+    (4, 40, 20480, 264),     # clusters that split the contraction, 32-row tiles
+    (1, 300, 20480, 512),    # the same with 128-row tiles
+    (64, 2048, 5120, 5120),  # one CTA per tile
+])
+@pytest.mark.parametrize("dtype", [BF, HF])
+def test_fp32_results_are_summed_in_short_pieces(E, R, K, N, dtype):
+    """In one piece, 20480 one-signed products would come out 1280 x 2^-25 = 3.8e-5 low, 5120 of them 9.5e-6; the
+    bounds are 1.2e-5 and 8.0e-6."""
+    g = gen(R)
+    counts = ragged_counts(E, R, 5)
+    off = offsets_of(counts)
+    x, w = one_signed(g, R, K, dtype=dtype), one_signed(g, E, N, K, dtype=dtype)
+    out = bm.grouped_mm(x, w, off, out_dtype=F32)
+    dx = bm.grouped_mm_dgrad(x, w.transpose(1, 2).contiguous(), off, out_dtype=F32)
+    status_ok()
+    want = torch.empty(R, N, dtype=D, device="cuda")
+    for e, a, b in spans(counts):
+        want[a:b] = x[a:b].to(D) @ w[e].to(D).t()
+    check(out, want, even_tol(want, 256, K), "out")
+    check(dx, want, even_tol(want, 256, K), "dx")
+
+
+@pytest.mark.parametrize("counts,N,K,piece", [
+    ([40000], 9456, 1016, 4096),      # 512-column tiles: 148 tiles of 256 columns on 74 pairs, 74 of 512
+    ([64, 40000], 4600, 1016, 4096),  # 144 and 72
+    ([40000, 3], 320, 192, 256),      # rows split over the pairs
+    ([12000] * 8, 2560, 256, 256),    # 256-column tiles: K has no second 256
+])
+def test_fp32_weight_gradients_are_summed_in_pieces(counts, N, K, piece):
+    """40000 one-signed rows in one piece would come out 2500 x 2^-25 = 7.5e-5 low, 12000 of them 2.2e-5; the bounds are
+    4.3e-5 in pieces of 4096 and 9.5e-6 (12000 rows) in pieces of 256.  Accumulated ones take one rounding more per
+    piece."""
+    g = gen(N)
+    R = sum(counts)
+    off = offsets_of(counts)
+    dy, x = one_signed(g, R, N), one_signed(g, R, K)
+    want = torch.empty(len(counts), N, K, dtype=D, device="cuda")
+    for e, a, b in spans(counts):
+        want[e] = dy[a:b].to(D).t() @ x[a:b].to(D)
+    dw = bm.grouped_mm_wgrad(dy, x, off, out_dtype=F32)
+    status_ok()
+    length = torch.tensor(counts, device="cuda")[:, None, None]
+    tol = torch.stack([even_tol(want[e], piece, c) for e, c in enumerate(counts)])
+    check(dw, want, tol, "dw")
+    before = torch.rand(len(counts), N, K, generator=g, device="cuda") * length
+    got = before.clone()
+    bm.grouped_mm_wgrad(dy, x, off, out=got, accumulate=True)
+    status_ok()
+    want = want + before.to(D)
+    check(got, want, tol + want * ((max(counts) // piece + 2) * 2.0 ** -24), "accumulated")
+
+
 def test_gradients_against_differences():
     """out is linear in x and in w: the change of sum(dy * out) along any direction is its gradient times
     that direction, exactly but for the roundings (fp32 results)."""
