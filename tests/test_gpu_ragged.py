@@ -358,6 +358,32 @@ def test_fp32_weight_gradients_are_summed_in_pieces(counts, N, K, piece):
     check(got, want, tol + want * ((max(counts) // piece + 2) * 2.0 ** -24), "accumulated")
 
 
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("counts,N,K", [([5107], 9456, 1016), ([64, 5000], 4600, 1016), ([64, 0, 0, 6001], 2296, 1016),
+                                        ([16384], 9456, 1016), ([0, 4097, 1, 63], 2296, 1016)])
+def test_weight_gradient_on_512_column_tiles(counts, N, K, dtype):
+    """Sizes whose 256-column tiles take two rounds of the 74 pairs and whose 512-column tiles take one, so that the
+    latter run (one round costs 1060 cycles per k-step, two 1380; of the last, with 17 k-steps per group, only the
+    16-bit result): one group, short and empty groups beside long ones, the longest single piece of fp16."""
+    E, R = len(counts), sum(counts)
+    g = gen(R)
+    dy, x = normal(g, R, N, dtype=dtype), normal(g, R, K, dtype=dtype)
+    off = offsets_of(counts)
+    v, mag = products(x, dy, torch.zeros(E, N, K, device="cuda"), counts)["dw"]
+    for out_dtype in (dtype, F32):
+        check(bm.grouped_mm_wgrad(dy, x, off, out_dtype=out_dtype), v,
+              half_step(v, out_dtype) + sum_tol(mag, max(counts), out_dtype), f"{out_dtype}")
+    before = torch.randn(E, N, K, generator=g, device="cuda")
+    dw = before.clone()
+    bm.grouped_mm_wgrad(dy, x, off, out=dw, accumulate=True)
+    want = before.to(D) + v
+    check(dw, want, half_step(want, F32) + sum_tol(mag + before.abs(), max(counts), F32), "accumulated")
+    for e, c in enumerate(counts):
+        if c == 0:
+            assert torch.equal(dw[e], before[e])
+    status_ok()
+
+
 def test_gradients_against_differences():
     """out is linear in x and in w: the change of sum(dy * out) along any direction is its gradient times
     that direction, exactly but for the roundings (fp32 results)."""
