@@ -847,6 +847,42 @@ def test_calls_that_follow_one_another(R, E):
         assert all(torch.equal(r.nan_to_num(), v.nan_to_num()) for r, v in zip(result, want))
 
 
+@pytest.mark.parametrize("R,E", [(1, 1), (40, 8), (700, 8)])
+def test_int8_calls_that_follow_one_another(R, E):
+    """Quantisers and products back to back over the same buffers: finite, and bit for bit what they give with a wait
+    behind each call."""
+    H, I, n = 512, 320, 16
+    g = gen(R + 7)
+    off = offsets_of(ragged_counts(E, R, 6, empty=0.0))
+    w8 = [torch.randint(-127, 128, (E, a, b), generator=g, device="cuda", dtype=torch.int8)
+          for a, b in ((I, H), (I, H), (H, I))]
+    cs = [torch.rand(E, a, generator=g, device="cuda") / 1000 + 1e-4 for a in (I, I, H)]
+    x, steps = torch.empty(R, H, dtype=BF, device="cuda"), normal(g, n, R, H)
+    q, s, hq, hs = bm.quant_i8_rows(steps[0]) + (torch.empty(R, I, dtype=torch.int8, device="cuda"),
+                                                 torch.empty(R, device="cuda"))
+    gate, up = (torch.empty(R, I, device="cuda") for _ in range(2))
+    out = torch.empty(n, R, H, device="cuda")
+
+    def run(sync):
+        out.zero_()
+        for i in range(n):
+            for f in (lambda: x.copy_(steps[i]), lambda: bm.quant_i8_rows(x, q, s),
+                      lambda: bm.grouped_mm_i8(q, s, w8[0], cs[0], off, out=gate),
+                      lambda: bm.grouped_mm_i8(q, s, w8[1], cs[1], off, out=up),
+                      lambda: bm.swiglu_i8(gate, up, hq, hs),
+                      lambda: bm.grouped_mm_i8(hq, hs, w8[2], cs[2], off, out=out[i])):
+                f()
+                if sync:
+                    torch.cuda.synchronize()
+        return out.clone()
+
+    want = run(True)
+    assert want.isfinite().all() and (want != 0).any(dim=2).all()
+    for _ in range(4):
+        assert torch.equal(run(False), want)
+    status_ok()
+
+
 def test_two_calls_at_once():
     """Products of different kernels on two streams, overlapping: each gives what it gives alone."""
     g = gen(61)
