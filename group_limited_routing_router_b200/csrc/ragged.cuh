@@ -1530,15 +1530,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kRwThreads, 1)
     if (warp == 1) tmem_dealloc_pair(tmem_base, 512);
 }
 
-// dw = (accumulate ? dw : 0) + the FP32 partial sums of `splits` splits in order, n values each.
+// dw = (accumulate ? dw : 0) + the FP32 partial sums of `splits` splits in order, n values each.  Where it
+// accumulates, groups without rows are left alone (a sum of zeros would turn -0 into 0); rows are only split where
+// few weights are, so the index of four values fits 32 bits.
 template <int TYPE>
 __global__ void __launch_bounds__(256) ragged_join_kernel(const float4 *__restrict__ part, int splits, int64_t n4,
                                                          int accumulate, void *__restrict__ out,
                                                          const int64_t *__restrict__ offsets, int E, int64_t R) {
+    const uint32_t per_group = static_cast<uint32_t>(n4) / static_cast<uint32_t>(E);
     const int e = threadIdx.x;  // E <= 256: bad offsets left the partial sums unwritten
     const bool bad = offsets && e < E && (offsets[e] < 0 || offsets[e + 1] < offsets[e] || offsets[e + 1] > R);
     if (__syncthreads_or(bad)) return;
     for (int64_t i = blockIdx.x * 256ll + threadIdx.x; i < n4; i += gridDim.x * 256ll) {
+        if (TYPE == BEAM_MOE_F32 && accumulate && offsets) {
+            const uint32_t g = static_cast<uint32_t>(i) / per_group;
+            if (offsets[g + 1] == offsets[g]) continue;
+        }
         float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
         for (int s = 0; s < splits; ++s) {
             const float4 v = __ldg(part + s * n4 + i);

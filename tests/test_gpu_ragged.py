@@ -245,6 +245,22 @@ def test_weight_gradient_accumulates(E, R, N, K):
         assert torch.equal(dw[3], before[3])
 
 
+@pytest.mark.parametrize("counts,N,K", [([0, 20000, 0], 192, 320), ([9000, 0], 64, 72), ([3, 0, 4], 192, 320),
+                                        ([0, 9000], 4600, 1016)])
+def test_an_expert_without_rows_keeps_every_bit(counts, N, K):
+    """Negative zeros, NaN and subnormals of its accumulated gradient, with rows split and not."""
+    g = gen(N)
+    off = offsets_of(counts)
+    dw = torch.randn(len(counts), N, K, generator=g, device="cuda")
+    dw[:, ::2, ::3], dw[:, 1::2, 1::3], dw[:, :, 2::3] = -0.0, float("nan"), -1e-42
+    before = dw.clone()
+    bm.grouped_mm_wgrad(normal(g, sum(counts), N), normal(g, sum(counts), K), off, out=dw, accumulate=True)
+    status_ok()
+    for e, c in enumerate(counts):
+        if c == 0:
+            assert torch.equal(dw[e].view(torch.int32), before[e].view(torch.int32))
+
+
 @pytest.mark.parametrize("dtype", [BF, HF])
 @pytest.mark.parametrize("counts", [[0, 5107, 300], [5107], [64, 0, 0, 6001]])
 def test_weight_gradient_of_long_groups(counts, dtype):
