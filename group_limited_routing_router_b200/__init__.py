@@ -749,7 +749,7 @@ def grouped_mm(x, w, offsets=None, out=None, out_dtype=None, stream=None) -> tor
 
     x [R, K] and w [E, N, K] bf16 or fp16 (or w [N, K] without offsets: one expert that takes every row);
     offsets [E + 1] int64 on the device (permute()'s); out [R, N] in x's type or fp32.  Rows of no expert
-    are not written."""
+    are not written.  Not recorded by autograd: its gradients are grouped_mm_dgrad and grouped_mm_wgrad."""
     ldx = _rows(x, "x", _HALF)
     device, dtype = x.device, x.dtype
     w = _weights3(w, "w", dtype, device)
@@ -827,7 +827,8 @@ def _codes(q, scale, R: int, K: int, device, stream):
 
 
 def quant_i8_rows(x, q=None, scale=None, stream=None):
-    """(q [R, K] int8, scale [R] fp32): scale = max|x[r]| / 127, q = x / scale to the nearest integer."""
+    """(q [R, K] int8, scale [R] fp32): scale = max|x[r]| / 127, q = x / scale to the nearest integer.  Not recorded
+    by autograd."""
     ldx = _rows(x, "x", TYPES)
     R, K = x.shape
     q, scale = _codes(q, scale, R, K, x.device, stream)
@@ -840,7 +841,7 @@ def grouped_mm_i8(q, row_scale, w, channel_scale, offsets=None, out=None, out_dt
     """grouped_mm of INT8 codes: out[r, n] = (q[r] . w[e, n]) * row_scale[r] * channel_scale[e, n].
 
     q [R, K] int8 and row_scale [R] fp32 (quant_i8_rows), w [E, N, K] int8 and channel_scale [E, N] fp32 (or
-    [N, K] and [N]); out [R, N] bf16 (default), fp16 or fp32."""
+    [N, K] and [N]); out [R, N] bf16 (default), fp16 or fp32.  Not recorded by autograd."""
     if not isinstance(q, torch.Tensor) or q.dim() != 2:
         raise TypeError("q must be a CUDA int8 matrix (there is no CPU path)")
     R, K = q.shape
@@ -862,7 +863,8 @@ def grouped_mm_i8(q, row_scale, w, channel_scale, offsets=None, out=None, out_dt
 
 
 def swiglu(g, u, out=None, stream=None) -> torch.Tensor:
-    """SiLU(g) * u over [R, I] (bf16, fp16 or fp32); `out` may be g or u."""
+    """SiLU(g) * u over [R, I] (bf16, fp16 or fp32); `out` may be g or u.  Not recorded by autograd: its gradients
+    are swiglu_backward."""
     ldg = _rows(g, "g", TYPES)
     R, I = size = g.shape
     device, types = g.device, (g.dtype,)
@@ -888,7 +890,8 @@ def swiglu_backward(dh, g, u, dg=None, du=None, stream=None):
 
 
 def swiglu_i8(g, u, q=None, scale=None, stream=None):
-    """quant_i8_rows(SiLU(g) * u) in one pass, the product kept in fp32: (q [R, I] int8, scale [R] fp32)."""
+    """quant_i8_rows(SiLU(g) * u) in one pass, the product kept in fp32: (q [R, I] int8, scale [R] fp32).  Not
+    recorded by autograd."""
     ldg = _rows(g, "g", TYPES)
     R, I = size = g.shape
     device, types = g.device, (g.dtype,)

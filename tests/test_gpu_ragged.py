@@ -993,3 +993,15 @@ def test_on_another_stream():
     side.synchronize()
     assert all(torch.equal(got[k], want[k]) for k in want)
     status_ok()
+
+
+def test_results_are_detached():
+    """Inputs that require gradients are taken; what comes back does not claim to have any."""
+    g = gen(81)
+    x, w = normal(g, 40, 64).requires_grad_(), normal(g, 32, 64).requires_grad_()
+    out = bm.grouped_mm(x, w)
+    h = bm.swiglu(out, out)
+    q, s = bm.quant_i8_rows(x)
+    for t in (out, h, s, bm.grouped_mm_dgrad(out, w), bm.grouped_mm_wgrad(out, x), *bm.swiglu_backward(h, out, out)):
+        assert not t.requires_grad and t.isfinite().all()
+    status_ok()

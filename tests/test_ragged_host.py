@@ -189,3 +189,8 @@ def test_partial_sums_are_released_to_the_cluster():
         behind = split.split("mbar_wait(" + bar)[1].split(";")[1:3]
         assert [s.strip() for s in behind] == ["if (!ok) break", "acquire_smem()"], bar
     assert "mbar_release_smem(mapa_shared(smem_u32(red_empty), lane))" in split and "mbar_arrive_async" not in split
+
+
+def test_docstrings_say_that_autograd_records_nothing():
+    for f in (bm.grouped_mm, bm.grouped_mm_i8, bm.swiglu, bm.quant_i8_rows, bm.swiglu_i8):
+        assert "not recorded by autograd" in " ".join(f.__doc__.split()).lower(), f.__name__
