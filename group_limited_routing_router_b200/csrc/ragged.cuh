@@ -1404,17 +1404,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kRwThreads, 1)
         // ---------------- helper: clears the rows behind the group in its last k-step
         const uint32_t full_lead = mapa_shared(smem_u32(full), 0);
         uint32_t steps = 0, phases = 0;  // k-steps up to this item's end; per stage, the phase of `tail`
+        long long limit = timeout;       // one for each item that it lets pass, and one for its own
         for (int item = pair, e = first; item < total; item += n_pairs) {
             const WgradItem it = wgrad_item<NB>(item, e, tile_start, p);
             if (it.rows == 0) continue;
             const uint32_t n_kb = static_cast<uint32_t>((it.rows + 63) / 64);
             steps += n_kb;
             const int v = it.rows - static_cast<int>(n_kb - 1) * 64;
-            if (!needs_clearing(v)) continue;
+            if (!needs_clearing(v)) {
+                limit += timeout;
+                continue;
+            }
             const uint32_t stage = (steps - 1) % kStages;
             const uint32_t phase = (phases >> stage) & 1u;
             phases ^= 1u << stage;
-            if (!mbar_wait(&tail[stage], phase, timeout)) break;
+            if (!mbar_wait(&tail[stage], phase, limit)) break;
+            limit = timeout;
             const uint32_t sa = smem_u32(smem + stage * C::kStage);
             const int lines = ((v + 15) & ~15) - v;  // 1..15 lines of 128 bytes per box
             // every box of the stage (those not loaded for this item hold nothing that is used)

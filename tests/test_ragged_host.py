@@ -175,6 +175,11 @@ def test_cleared_rows_are_released_to_the_cluster():
         code = f.read()
     helper = code.split("helper: clears the rows behind the group")[1].split("epilogue: lanes = rows n")[0]
     assert "mbar_release_smem(full_lead" in helper and "mbar_arrive_async" not in helper
+    # it lets items pass that have nothing to clear, so what it waits for may be many items away: a call of 640000 rows
+    # by 65536 x 65536 runs for some 4 s, the limit of one wait is 2e9 cycles
+    passes = "".join(helper.split())
+    assert "if(!needs_clearing(v)){limit+=timeout;continue;}" in passes
+    assert "mbar_wait(&tail[stage],phase,limit))break;limit=timeout;" in passes
     issuer = code.split("ragged_wgrad_kernel(")[1].split("MMA issuer for the pair")[1].split("helper: clears")[0]
     assert "if (needs_clearing(it.rows - kb * 64)) acquire_smem();" in issuer
 
