@@ -297,9 +297,10 @@ __device__ __forceinline__ void pack_chunk(int sub, float rs, const float (&ch)[
 // Stores a packed chunk of 16 rows from row c on.  q: this warp's 32 of the 128 features from mt0 on (M is a
 // multiple of 8); stage: its four warps' two buffers, between which `flip` alternates, so that one barrier per
 // chunk orders a buffer's writes after the reads of two chunks ago.  live: false after a wait has timed out.  TIGHT:
-// a row's 16 bytes at a time, where two tiles' packed sums leave few registers (NA = 2, 64 groups of ~256 rows, input
-// gradient of 5120 x 2560: 415 -> 407 us); both rows together where the stores are the bound (NA = 1, 45231 rows,
-// 224 x 4328: 5 to 15% less).
+// a row's 16 bytes at a time, where two tiles' packed sums leave few registers (NA = 2: 4 bytes spilled, 120 with both
+// rows together; the time is the same: 64 groups of ~256 rows, input gradients, 421 and 444 us against 433 and 435;
+// 256 of ~128, 1178 against 1157); both rows together where the stores are the bound (NA = 1, 45231 rows, 224 x 4328:
+// 5 to 15% less).
 template <bool TIGHT>
 __device__ __forceinline__ void store_chunk(const RaggedParams &p, const RaggedItem &it, int c, int mt0, int q, int sub,
                                             uint32_t stage, int flip, bool live, const uint32_t (&pk)[8]) {

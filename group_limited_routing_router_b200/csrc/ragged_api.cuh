@@ -139,7 +139,9 @@ int segment_steps(bool i8, int out_type, int n_kb) {
 // The wide tiles sum 16-bit results in one segment where that loses at most an eighth of the result's half
 // step: length / 16 x 2^-25 <= 2^-12 (bf16) or 2^-15 (fp16).
 bool one_segment_ok(int dtype, int64_t length) { return length <= (dtype == BEAM_MOE_BF16 ? 131072 : 16384); }
-// wgrad's wide tiles flush fp32 results every 4096 rows: 256 instructions, 2^-17 at most.
+// wgrad's wide tiles flush fp32 results every 4096 rows: 256 instructions, 2^-17 at most, against 2^-21 of the 256-column
+// tiles.  Flushed every 1024 rows (2^-19) they are no faster than those (fp32, 8 groups of 8192 rows, 5120 x 2560: 1.51
+// ms; every 1024 rows 1.82; 256-column tiles 1.86).
 constexpr int kFlushSteps = 64;
 
 uint32_t ragged_idesc(bool i8, int dtype, int M, bool a_mn, bool b_mn) {
@@ -341,11 +343,14 @@ int ragged_product(const RaggedCall &c, cudaStream_t s) {
 }
 
 // Splits of wgrad's rows: one where the result's tiles fill the 74 pairs of a 148-SM B200; else enough to
-// fill them, of at least 512 rows of a mean group each.  Pure host arithmetic.
+// fill them, of at least 512 rows of a mean group each.  The number of pairs is a constant, because the workspace's size
+// is asked for without a device and has to be the same when the call is made; with other pairs the result is the same
+// and only the time differs.
 int wgrad_splits(int E, int64_t R, int K, int N) {
     const int64_t tiles = static_cast<int64_t>(E) * ((N + 255) / 256) * ((K + 255) / 256);
     const int64_t by_rows = R / E / 512;
-    return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(74 / tiles, by_rows), 64)));
+    constexpr int64_t kSplitPairs = 74;
+    return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(kSplitPairs / tiles, by_rows), 64)));
 }
 // Whether wgrad's 256 x 512 tiles run: where their rounds come out shorter for a mean group, with the cycles
 // measured per k-step (~690 for 256 columns, ~1060 for 512, both bound by L2) and per item (decoding and
