@@ -109,8 +109,9 @@ __device__ __forceinline__ void mbar_arrive_async(uint32_t bar_cluster) {
 }
 
 // The same behind a release at cluster scope of shared memory alone: what the warp has read there may be overwritten
-// by whoever acquires it, and what it has written (and fenced for the async proxy) is seen.  wgrad, 256 groups of ~78 rows, 512 x 512: 38 us as without any
-// release, 49 with one of all memory (64 groups of 128 rows, 5120 x 2560: 389 against 431).
+// by whoever acquires it, and what it has written (and fenced for the async proxy) is seen.  wgrad, 256 groups of ~78
+// rows, 512 x 512: 38 us as without any release, 49 with one of all memory (64 groups of 128 rows, 5120 x 2560: 389
+// against 431).
 __device__ __forceinline__ void mbar_release_smem(uint32_t bar_cluster) {
     asm volatile(
         "fence.release.sync_restrict::shared::cta.cluster;\n\t"
